@@ -170,6 +170,116 @@ void seqsum_plan_destroy(seqsum_plan *plan);
 int seqsum_f64_planned(seqsum_plan *plan, const double *x, int64_t n, double s0, double *out,
                        cudaStream_t stream);
 
+/* ---- Sums that decide: tokens, log-probabilities, the norm of gradients.
+ *
+ * Sums over rows of logits and over all gradients of a model, in the manner
+ * of the sums above: their bits are defined.  The calls below enqueue on
+ * `stream` and return without waiting, allocate nothing (seqsum_tensors_create
+ * apart), use no workspace of a stream and may be captured into graphs.
+ * seqsum_get_stats() does not cover them. */
+
+enum { SEQSUM_FP32 = 0, SEQSUM_FP16 = 1, SEQSUM_BF16 = 2 };
+
+/* The largest number of rows of one call, and of numbers in a row. */
+#define SEQSUM_MAX_ROWS (1 << 27)
+#define SEQSUM_MAX_VOCAB (1 << 24)
+
+/* The settings of seqsum_sample_tokens: one value for all rows, or, where the
+ * pointer beside it is not null, one for each row (device). */
+typedef struct {
+  float temperature;          /* <= 0: the lowest index of the largest logit */
+  int32_t top_k;              /* <= 0: off */
+  float top_p;                /* >= 1: off */
+  float min_p;                /* <= 0: off; above 1 as 1 */
+  const float *temperatures;
+  const int32_t *top_ks;
+  const float *top_ps;
+  const float *min_ps;
+} seqsum_sampling;
+
+/* One token a row of logits, from a given random number each.  A token is
+ * where a running sum passes a threshold, so two orders of the sum can give
+ * two tokens; here every sum is one of integers:
+ *   m = the row's maximum (NaN counts as -inf), c = log2(e) / temperature
+ *   d_i = (x_i - m) * c, w_i = 2^31 * 2^d_i rounded to an integer
+ *   (d = 0 at the maximum; fp32 operations, each rounded)
+ *   order: larger d first, among equals the lower index
+ *   top-k: the first k of the order; M = their sum of w
+ *   top-p: an entry is kept where the sum before it is below floor(P * M / 2^32),
+ *     P = floor(top_p * 2^32); the first one always
+ *   min-p: an entry is kept where w >= 2^31 * min_p, rounded
+ *   Z = the sum of the kept; the token is the lowest index at which the sum of
+ *   the kept up to it is above floor(U * Z / 2^32), U = floor(u * 2^32)
+ * and logps[row] = ln(w_token / Z), taken from d.  A row with nothing above
+ * -inf gives token -1 and logp -inf; a greedy row gives logp 0.
+ *   logits      device, rows x vocab of `dtype`, a row's numbers one after
+ *               another (any alignment of the type), read only
+ *   row_stride  numbers from one row's start to the next
+ *   u           device, one number in [0, 1) a row (others are taken as the nearest)
+ *   sampling    host, read during the call
+ *   tokens, logps  device, one a row, written
+ * Returns SEQSUM_OK, SEQSUM_EINVAL or SEQSUM_ECUDA. */
+int seqsum_sample_tokens(const void *logits, int32_t dtype, int64_t rows, int64_t vocab, int64_t row_stride,
+                         const float *u, const seqsum_sampling *sampling, int64_t *tokens, float *logps,
+                         cudaStream_t stream);
+
+/* For each row, lses[row] = ln sum exp(x_i) and logps[row] = x_token - lse.
+ * A token outside [0, vocab) marks an unused row (padding): its logp is 0.  A
+ * row of nothing but -inf has lse -inf and logp -inf; a NaN or +inf in a row
+ * makes both NaN.  A row's results do not depend on the other rows. */
+int seqsum_token_logprob(const void *logits, int32_t dtype, int64_t rows, int64_t vocab, int64_t row_stride,
+                         const int64_t *tokens, float *logps, float *lses, cudaStream_t stream);
+
+/* As seqsum_token_logprob, and the gradient of sum_r dlogps[r] * logps[r]
+ * with respect to the logits, in the logits' type:
+ *   dlogits_ri = dlogps[r] * ([i = token_r] - exp(x_ri - lse_r))
+ * An unused row's gradient, and that of a row of nothing but -inf, is 0.
+ *   dlogits  device, written; the logits themselves (with their stride) or
+ *            memory apart from them
+ * The logits are read once. */
+int seqsum_token_logprob_grad(const void *logits, int32_t dtype, int64_t rows, int64_t vocab, int64_t row_stride,
+                              const int64_t *tokens, const float *dlogps, void *dlogits, int64_t drow_stride,
+                              float *logps, float *lses, cudaStream_t stream);
+
+/* The same gradient from the lses of an earlier call. */
+int seqsum_token_logprob_backward(const void *logits, int32_t dtype, int64_t rows, int64_t vocab, int64_t row_stride,
+                                  const int64_t *tokens, const float *dlogps, const float *lses, void *dlogits,
+                                  int64_t drow_stride, cudaStream_t stream);
+
+/* One of many tensors: `count` numbers of `dtype` at `data` (device; any
+ * alignment of the type).  `out`: where seqsum_tensors_clip writes them, of
+ * out_dtype, apart from every `data`; or null for `data` itself. */
+typedef struct {
+  const void *data;
+  void *out;
+  int64_t count;
+  int32_t dtype, out_dtype;
+} seqsum_tensor;
+
+/* A list of tensors on the current device (opaque): a table of their
+ * addresses and sizes, kept on the device from call to call.  The tensors
+ * stay the caller's and have to outlive the list's calls. */
+typedef struct seqsum_tensors seqsum_tensors;
+
+/* Makes a list of n tensors (host array).  Allocates and waits for its copy.
+ * Returns SEQSUM_OK, SEQSUM_EINVAL, SEQSUM_ENOMEM or SEQSUM_ECUDA. */
+int seqsum_tensors_create(const seqsum_tensor *tensors, int32_t n, seqsum_tensors **out);
+
+/* Waits for the device and frees the list.  A null list is ignored. */
+void seqsum_tensors_destroy(seqsum_tensors *tensors);
+
+/* *norm = scale * sqrt(the sum of the squares of all numbers of the list).
+ * The order of the sum is fixed by the tensors' sizes and types; squares that
+ * leave fp32's range are taken in double.  No tensors: 0.  Calls on one list
+ * must be ordered (one stream, or synchronised). */
+int seqsum_tensors_norm(seqsum_tensors *tensors, float scale, float *norm, cudaStream_t stream);
+
+/* As seqsum_tensors_norm, and every number g written as
+ *   g * (scale * min(1, max_norm / (*norm + 1e-6)))
+ * (fp32, rounded once to the out's type) to its tensor's out.  A norm of NaN
+ * makes the factor NaN, an infinite one makes it 0. */
+int seqsum_tensors_clip(seqsum_tensors *tensors, float max_norm, float scale, float *norm, cudaStream_t stream);
+
 /* Counters accumulated on the device by the calls since the last
  * seqsum_get_stats() on the same (device, stream) workspace as the most
  * recent call of this process. */

@@ -20,7 +20,20 @@ from . import build as _build
 __all__ = ["seqsum_f64", "seqsum_f64_static", "seqsum_f64_batched", "seqsum_f64_batched_sized", "get_stats",
            "debug_set_plan", "debug_set_fault", "debug_counters", "release_workspace", "version", "lib", "lib_path",
            "seqsum_f64_strided", "SeqsumPlan",
-           "SeqsumError"]
+           "SeqsumError", "sample_tokens", "token_logprob", "token_logprob_grad", "token_logprob_backward", "TensorList"]
+
+# loaded on first use, so that the package itself imports without torch
+_OPERATORS = ("sample_tokens", "token_logprob", "token_logprob_grad", "token_logprob_backward", "TensorList")
+
+
+def __getattr__(name):
+    if name in _OPERATORS:
+        from . import operators
+        for op in _OPERATORS:
+            globals()[op] = getattr(operators, op)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
 
 _lock = threading.Lock()
 _lib = None

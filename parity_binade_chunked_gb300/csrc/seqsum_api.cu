@@ -8,12 +8,14 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include <atomic>
 #include <map>
 #include <mutex>
 #include <new>
 #include <utility>
 
 #include "../../include/seqsum.h"
+#include "row_slice.cuh"
 #include "seqsum_internal.cuh"
 
 namespace {
@@ -260,6 +262,23 @@ int batched_impl(const double *x, int64_t x_len, const int64_t *offsets, int32_t
 }
 
 }  // namespace
+
+namespace sq {
+
+// for the other translation units' entries (row_slice.cuh)
+int note_cuda(cudaError_t e) { return cuda_fail(e); }
+
+int multiprocessors() {
+  static std::atomic<int> known[64];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0 && cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
+    known[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+}  // namespace sq
 
 extern "C" {
 

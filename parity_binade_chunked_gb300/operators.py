@@ -1,0 +1,267 @@
+"""Sums that decide, on one GB300: tokens drawn from logits, their
+log-probabilities and gradients, the norm of many tensors and clipping by it.
+
+The same thin binding as the package's: arguments are checked and passed on,
+every computation is a kernel of libseqsum.so.  Work is enqueued on the
+current torch stream unless a stream is given; results are ready once that
+stream reaches them.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import SeqsumError, _check, lib
+
+_DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+_SETTINGS = (("temperature", torch.float32), ("top_k", torch.int32), ("top_p", torch.float32), ("min_p", torch.float32))
+
+
+class _Sampling(ctypes.Structure):
+    _fields_ = [("temperature", ctypes.c_float), ("top_k", ctypes.c_int32), ("top_p", ctypes.c_float),
+                ("min_p", ctypes.c_float), ("temperatures", ctypes.c_void_p), ("top_ks", ctypes.c_void_p),
+                ("top_ps", ctypes.c_void_p), ("min_ps", ctypes.c_void_p)]
+
+
+class _Tensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("out", ctypes.c_void_p), ("count", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+
+
+_lib = None
+
+
+def _entries():
+    """The library, with the argument types of the entries that this module calls."""
+    global _lib
+    if _lib is not None:
+        return _lib
+    L = lib()
+    vp, i64, i32, f = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
+    rows = [vp, i32, i64, i64, i64]
+    for name, args in (("sample_tokens", rows + [vp, ctypes.POINTER(_Sampling), vp, vp, vp]),
+                       ("token_logprob", rows + [vp, vp, vp, vp]),
+                       ("token_logprob_grad", rows + [vp, vp, vp, i64, vp, vp, vp]),
+                       ("token_logprob_backward", rows + [vp, vp, vp, vp, i64, vp]),
+                       ("tensors_create", [ctypes.POINTER(_Tensor), i32, ctypes.POINTER(vp)]),
+                       ("tensors_norm", [vp, f, vp, vp]),
+                       ("tensors_clip", [vp, f, f, vp, vp])):
+        fn = getattr(L, "seqsum_" + name)
+        fn.argtypes, fn.restype = args, ctypes.c_int
+    L.seqsum_tensors_destroy.argtypes, L.seqsum_tensors_destroy.restype = [vp], None
+    _lib = L
+    return L
+
+
+def _call(device, stream, entry, *args):
+    """Calls an entry on `device`, its last argument the stream's handle."""
+    fn = getattr(_entries(), entry)
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, handle))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, handle))
+
+
+def _new(shape, dtype, device, stream):
+    """An output's memory; where another stream than the current one writes it, the allocator is told."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
+                        torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream), device=device))
+    return t
+
+
+def _logits(x, name="logits"):
+    """rows, vocab, row stride, dtype code of a 2-D tensor whose rows are contiguous."""
+    if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dtype in _DTYPES and x.dim() == 2):
+        raise TypeError(f"{name} must be a 2-D CUDA tensor of float32, float16 or bfloat16")
+    rows, vocab = x.shape
+    stride, unit = x.stride()
+    if unit != 1 and vocab > 1:
+        raise TypeError(f"{name} must have contiguous rows (stride 1 in the last dimension)")
+    return rows, vocab, stride if rows > 1 else vocab, _DTYPES[x.dtype]
+
+
+def _vector(t, name, rows, dtype, device):
+    if not (isinstance(t, torch.Tensor) and t.device == device and t.dtype == dtype and t.is_contiguous()
+            and t.shape == (rows,)):
+        raise TypeError(f"{name} must be a contiguous {dtype} tensor of {rows} entries on {device}")
+    return t.data_ptr()
+
+
+def sample_tokens(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tokens=None, logps=None, stream=None):
+    """One token a row of `logits` (rows x vocab) from the random numbers `u`
+    (float32, one a row, in [0, 1)): (tokens int64, logps float32).
+
+    Each setting is a number for all rows or a tensor of one a row
+    (temperature, top_p, min_p float32, top_k int32).  temperature <= 0 is
+    greedy; top_k <= 0, top_p >= 1 and min_p <= 0 are off.  The filters apply
+    in the order top-k, top-p, min-p.  The sums are integers: a row's token
+    does not depend on the batch it is in."""
+    rows, vocab, stride, dtype = _logits(logits)
+    device = logits.device
+    s = _Sampling()
+    for (name, kind), v in zip(_SETTINGS, (temperature, top_k, top_p, min_p)):
+        if isinstance(v, torch.Tensor):
+            setattr(s, name + "s", _vector(v, name, rows, kind, device))
+        elif v != v:
+            raise ValueError(f"{name} is NaN")
+        else:
+            setattr(s, name, min(max(int(v), 0), 2 ** 31 - 1) if name == "top_k" else float(v))
+    up = _vector(u, "u", rows, torch.float32, device)
+    tokens = _new(rows, torch.int64, device, stream) if tokens is None else tokens
+    logps = _new(rows, torch.float32, device, stream) if logps is None else logps
+    _call(device, stream, "seqsum_sample_tokens", logits.data_ptr(), dtype, rows, vocab, stride, up, s,
+          _vector(tokens, "tokens", rows, torch.int64, device), _vector(logps, "logps", rows, torch.float32, device))
+    return tokens, logps
+
+
+def token_logprob(logits, tokens, logps=None, lses=None, stream=None):
+    """(logps, lses), float32: the log-probability of each row's token and the
+    row's log of the sum of exponentials.  A token outside [0, vocab) marks an
+    unused row: its logp is 0."""
+    rows, vocab, stride, dtype = _logits(logits)
+    device = logits.device
+    tp = _vector(tokens, "tokens", rows, torch.int64, device)
+    logps = _new(rows, torch.float32, device, stream) if logps is None else logps
+    lses = _new(rows, torch.float32, device, stream) if lses is None else lses
+    _call(device, stream, "seqsum_token_logprob", logits.data_ptr(), dtype, rows, vocab, stride, tp,
+          _vector(logps, "logps", rows, torch.float32, device), _vector(lses, "lses", rows, torch.float32, device))
+    return logps, lses
+
+
+def _gradient(out, logits, stream):
+    """The gradient's tensor and its row stride: apart from the logits, or the logits themselves."""
+    if out is None:
+        out = _new(logits.shape, logits.dtype, logits.device, stream)
+    rows, vocab, stride, _ = _logits(out, "out")
+    if out.shape != logits.shape or out.dtype != logits.dtype or out.device != logits.device:
+        raise TypeError("out must have the logits' shape, type and device")
+    if rows > 1 and stride < vocab:
+        raise TypeError("out's rows overlap")
+    return out, stride
+
+
+def token_logprob_grad(logits, tokens, dlogps, out=None, logps=None, lses=None, stream=None):
+    """(dlogits, logps, lses): token_logprob and, from the same read of the
+    logits, the gradient of (dlogps * logps).sum() with respect to them.
+    `out` may be the logits."""
+    rows, vocab, stride, dtype = _logits(logits)
+    device = logits.device
+    tp = _vector(tokens, "tokens", rows, torch.int64, device)
+    gp = _vector(dlogps, "dlogps", rows, torch.float32, device)
+    out, ostride = _gradient(out, logits, stream)
+    logps = _new(rows, torch.float32, device, stream) if logps is None else logps
+    lses = _new(rows, torch.float32, device, stream) if lses is None else lses
+    _call(device, stream, "seqsum_token_logprob_grad", logits.data_ptr(), dtype, rows, vocab, stride, tp, gp,
+          out.data_ptr(), ostride, _vector(logps, "logps", rows, torch.float32, device),
+          _vector(lses, "lses", rows, torch.float32, device))
+    return out, logps, lses
+
+
+def token_logprob_backward(logits, tokens, dlogps, lses, out=None, stream=None):
+    """dlogits: the gradient of (dlogps * logps).sum() with respect to the
+    logits, from the lses that token_logprob returned.  `out` may be the logits."""
+    rows, vocab, stride, dtype = _logits(logits)
+    device = logits.device
+    tp = _vector(tokens, "tokens", rows, torch.int64, device)
+    gp = _vector(dlogps, "dlogps", rows, torch.float32, device)
+    lp = _vector(lses, "lses", rows, torch.float32, device)
+    out, ostride = _gradient(out, logits, stream)
+    _call(device, stream, "seqsum_token_logprob_backward", logits.data_ptr(), dtype, rows, vocab, stride, tp, gp, lp,
+          out.data_ptr(), ostride)
+    return out
+
+
+def _dense(t):
+    """Whether the tensor's numbers fill their memory without gaps or overlaps, in some order of its dimensions."""
+    if t.is_contiguous():
+        return True
+    at = 1
+    for stride, size in sorted((s, n) for s, n in zip(t.stride(), t.shape) if n != 1):
+        if stride != at:
+            return False
+        at *= size
+    return True
+
+
+class TensorList:
+    """Many tensors as one: their norm, and clipping by it
+    (seqsum_tensors_create / _norm / _clip / _destroy).
+
+    tensors  CUDA tensors (float32, float16, bfloat16, mixed as they come) of
+             one device, dense in memory (contiguous or permuted)
+    outs     where clip() writes: as many tensors, of the same shapes and
+             layouts, of their own types; None: the tensors themselves
+    The list keeps a table of addresses on the device: make a new one when a
+    tensor is replaced by another.  Calls on one list must be ordered."""
+
+    def __init__(self, tensors, outs=None):
+        self._h = None
+        tensors = list(tensors)
+        outs = [None] * len(tensors) if outs is None else list(outs)
+        if len(outs) != len(tensors):
+            raise ValueError("outs must be as many as tensors")
+        table = (_Tensor * max(len(tensors), 1))()
+        device = next((t.device for t in tensors if isinstance(t, torch.Tensor) and t.is_cuda), None)
+        if device is None:
+            device = torch.device("cuda", torch.cuda.current_device())
+        for entry, t, o in zip(table, tensors, outs):
+            if not (isinstance(t, torch.Tensor) and t.is_cuda and t.device == device and t.dtype in _DTYPES
+                    and _dense(t)):
+                raise TypeError("tensors must be dense CUDA tensors of float32, float16 or bfloat16 on one device")
+            if o is not None and not (isinstance(o, torch.Tensor) and o.device == device and o.dtype in _DTYPES
+                                      and o.shape == t.shape
+                                      and (o.stride() == t.stride() or (o.is_contiguous() and t.is_contiguous()))):
+                raise TypeError("outs must have their tensors' shapes, layouts and device")
+            entry.data, entry.count, entry.dtype = t.data_ptr(), t.numel(), _DTYPES[t.dtype]
+            if o is not None:
+                entry.out, entry.out_dtype = o.data_ptr(), _DTYPES[o.dtype]
+        self._keep = (tensors, outs)
+        self._device = device
+        h = ctypes.c_void_p()
+        with torch.cuda.device(device):
+            _check(_entries().seqsum_tensors_create(table, len(tensors), ctypes.byref(h)))
+        self._h = h
+
+    def _out(self, out, stream):
+        if self._h is None:
+            raise SeqsumError("seqsum: the list was closed")
+        if out is None:
+            out = _new(1, torch.float32, self._device, stream)
+        return out, _vector(out, "out", 1, torch.float32, self._device)
+
+    def norm(self, scale: float = 1.0, out=None, stream=None):
+        """scale * the 2-norm of all numbers of the list (a 1-element float32 tensor)."""
+        out, p = self._out(out, stream)
+        _call(self._device, stream, "seqsum_tensors_norm", self._h, float(scale), p)
+        return out
+
+    def clip(self, max_norm: float, scale: float = 1.0, out=None, stream=None):
+        """Writes every number times scale * min(1, max_norm / (norm + 1e-6))
+        and returns the norm (of the scaled numbers, before clipping)."""
+        out, p = self._out(out, stream)
+        _call(self._device, stream, "seqsum_tensors_clip", self._h, float(max_norm), float(scale), p)
+        return out
+
+    def close(self):
+        if self._h is not None:
+            _entries().seqsum_tensors_destroy(self._h)
+        self._h = self._keep = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
