@@ -19,7 +19,6 @@ namespace {
 using namespace row;
 
 constexpr float kLog2e = 1.44269504f;
-constexpr float kLn2 = 0.69314718f;
 constexpr float kUnit = 274877906944.0f;             // 2^38: at most 2^22 vectors of at most 4, or 2^21 of 8
 constexpr uint64_t kBad = 1ull << 63;                // marks a sum with something in it that is no number
 
@@ -41,8 +40,76 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-template <typename T, int KV, int NT, bool kGrad>
-__global__ __launch_bounds__(NT) void logprob_kernel(const LogprobArgs a) {
+// exp(v - base) of a vector's numbers: the largest one's is exactly 1 where base is it.
+template <int kE>
+__device__ __forceinline__ void exps(const float *v, float base, float *y) {
+  const uint64_t b = pair(-base, -base), l = pair(kLog2e, kLog2e);
+#pragma unroll
+  for (int e = 0; e < kE; e += 2) {
+    float p, q;
+    split(mul2(add2(pair(v[e], v[e + 1]), b), l), p, q);
+    y[e] = ex2(p), y[e + 1] = ex2(q);
+  }
+}
+
+// The sum of a slice's exponentials in units of 2^-38; `bad` where one is no number.
+template <typename S>
+__device__ __forceinline__ uint64_t sum_exps(const S &x, float base, bool &bad) {
+  uint64_t sum = 0;
+  float check = 0.0f;
+  x.each([&](int, const float *v) {
+    float s[S::kE];
+    exps<S::kE>(v, base, s);
+    uint64_t t[S::kE / 2];
+#pragma unroll
+    for (int e = 0; e < S::kE / 2; e++) t[e] = pair(s[e], s[e + S::kE / 2]);
+#pragma unroll
+    for (int o = S::kE / 4; o; o >>= 1)
+#pragma unroll
+      for (int e = 0; e < o; e++) t[e] = add2(t[e], t[e + o]);
+    float p, q;
+    split(t[0], p, q);
+    p += q;
+    check += p;
+    sum += __float2ull_rn(p * kUnit);   // (0 for NaN)
+  });
+  bad = !(check < INFINITY);
+  return sum;
+}
+
+// Writes a slice's gradient: coef * exponential, and `g` more at the token.
+template <typename S, typename T>
+__device__ __forceinline__ void write_gradient(const S &x, float base, T *d, bool aligned, float coef, float g,
+                                               int64_t token) {
+  const int32_t token_vec = (int32_t)((token + x.off) / S::kE);
+  const uint64_t c = pair(coef, coef);
+  x.each([&](int k, const float *v) {
+    float y[S::kE];
+    exps<S::kE>(v, base, y);
+#pragma unroll
+    for (int e = 0; e < S::kE; e += 2) split(mul2(pair(y[e], y[e + 1]), c), y[e], y[e + 1]);
+    if (x.first + 32 * k == token_vec) {
+#pragma unroll
+      for (int e = 0; e < S::kE; e++)
+        if (x.index(k, e) == token) y[e] += g;
+    }
+    x.write(d, aligned, k, y);
+  });
+}
+
+template <typename S, typename T>
+__device__ __forceinline__ void write_zeros(const S &x, T *d, bool aligned) {
+  float y[S::kE] = {};
+  for (int k = 0; k < x.steps; k++) x.write(d, aligned, k, y);
+}
+
+template <typename T>
+__device__ __forceinline__ bool same_alignment(const T *d, int32_t off) {
+  return (reinterpret_cast<uintptr_t>(d) & 15) / sizeof(T) == (uintptr_t)off;
+}
+
+template <typename T, int KV, int NT, int kCtas, bool kGrad>
+__global__ __launch_bounds__(NT, kCtas) void logprob_kernel(const LogprobArgs a) {
   __shared__ uint64_t box[2][kMaxCluster];
   __shared__ uint64_t part[NT / 32];
   __shared__ float pmax[NT / 32];
@@ -56,35 +123,20 @@ __global__ __launch_bounds__(NT) void logprob_kernel(const LogprobArgs a) {
   const int64_t token = a.tokens[row];
   const bool used = token >= 0 && token < a.vocab;
   const float xt = used ? Elem<T>::load(p + token) : 0.0f;   // before a gradient in place overwrites it
+  const float dlogp = kGrad ? a.dlogps[row] : 0.0f;
 
-  float m = -INFINITY;
-  x.each([&](int, const float *v) {
-#pragma unroll
-    for (int e = 0; e < x.kE; e++) m = fmaxf(m, v[e]);
-  });
-  m = warp_max(m);
+  float m = warp_max(x.largest());
   if (lane == 0) pmax[warp] = m;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < NT / 32; i++) m = fmaxf(m, pmax[i]);
   cluster_post(__float_as_uint(m), box[0], rank, size);
   for (uint32_t r = 0; r < size; r++) m = fmaxf(m, __uint_as_float((uint32_t)box[0][r]));
-  // a row of nothing but -inf: every exponential is 0 (of NaN: m is -inf, but the sum is NaN)
+  // a row of nothing but -inf: every exponential is 0 (with NaN beside them: m is -inf, but the sum is NaN)
   const float base = m == -INFINITY ? 0.0f : m;
 
-  uint64_t sum = 0;
-  bool bad = false;   // some exponential is no number
-  x.each([&](int, const float *v) {
-    float s[x.kE];
-#pragma unroll
-    for (int e = 0; e < x.kE; e++) s[e] = ex2((v[e] - base) * kLog2e);
-#pragma unroll
-    for (int o = x.kE / 2; o; o >>= 1)
-#pragma unroll
-      for (int e = 0; e < o; e++) s[e] += s[e + o];
-    bad |= !(s[0] < INFINITY);
-    sum += __float2ull_rn(s[0] * kUnit);   // (0 for NaN)
-  });
+  bool bad;
+  uint64_t sum = sum_exps(x, base, bad);
   bad = __any_sync(~0u, bad);
   sum = warp_sum(sum);
   if (lane == 0) part[warp] = sum | (bad ? kBad : 0);
@@ -96,27 +148,18 @@ __global__ __launch_bounds__(NT) void logprob_kernel(const LogprobArgs a) {
   all = flag = 0;
   for (uint32_t r = 0; r < size; r++) all += box[1][r] & ~kBad, flag |= box[1][r] & kBad;
   const float s = flag ? NAN : (float)all * (1.0f / kUnit);
-  const float ln = logf(s);
+  const bool nothing = m == -INFINITY && !flag;
   if (rank == 0 && threadIdx.x == 0) {
+    const float ln = logf(s);
     a.lses[row] = base + ln;
-    a.logps[row] = used ? (m == -INFINITY && !flag ? -INFINITY : (xt - base) - ln) : 0.0f;
+    a.logps[row] = used ? (nothing ? -INFINITY : (xt - base) - ln) : 0.0f;
   }
   if constexpr (kGrad) {
     T *d = static_cast<T *>(a.dlogits) + row * a.dstride;
-    const bool aligned = (reinterpret_cast<uintptr_t>(d) & 15) / sizeof(T) == (uintptr_t)x.off;
-    const bool zero = !used || (m == -INFINITY && !flag);
-    const float g = zero ? 0.0f : a.dlogps[row];
-    const float coef = -__fdiv_rn(g, s);
-    x.each([&](int k, const float *v) {
-      float y[x.kE];
-#pragma unroll
-      for (int e = 0; e < x.kE; e++) {
-        y[e] = ex2((v[e] - base) * kLog2e) * coef;
-        if (x.index(k, e) == token) y[e] += g;
-        if (zero) y[e] = 0.0f;
-      }
-      x.write(d, aligned, k, y);
-    });
+    const bool aligned = same_alignment(d, x.off);
+    const float coef = -__fdiv_rn(dlogp, s);
+    if (!used || nothing) write_zeros(x, d, aligned);
+    else write_gradient(x, base, d, aligned, coef, dlogp, token);
   }
 }
 
@@ -130,24 +173,15 @@ __global__ __launch_bounds__(NT) void backward_kernel(const LogprobArgs a) {
   const int64_t token = a.tokens[row];
   const bool used = token >= 0 && token < a.vocab;
   const float lse = a.lses_in[row], g = used ? a.dlogps[row] : 0.0f;
-  const bool zero = !used || lse == -INFINITY;
   T *d = static_cast<T *>(a.dlogits) + row * a.dstride;
-  const bool aligned = (reinterpret_cast<uintptr_t>(d) & 15) / sizeof(T) == (uintptr_t)x.off;
-  x.each([&](int k, const float *v) {
-    float y[x.kE];
-#pragma unroll
-    for (int e = 0; e < x.kE; e++) {
-      y[e] = ex2((v[e] - lse) * kLog2e) * -g;
-      if (x.index(k, e) == token) y[e] += g;
-      if (zero) y[e] = 0.0f;
-    }
-    x.write(d, aligned, k, y);
-  });
+  const bool aligned = same_alignment(d, x.off);
+  if (!used || lse == -INFINITY) write_zeros(x, d, aligned);
+  else write_gradient(x, lse, d, aligned, -g, g, token);
 }
 
-template <typename T, int KV, int NT, bool kGrad>
+template <typename T, int KV, int NT, int kCtas, bool kGrad>
 int run_logprob(const LogprobArgs &a, int size, cudaStream_t stream) {
-  const cudaError_t e = launch_rows(logprob_kernel<T, KV, NT, kGrad>, a, a.rows, size, NT, stream);
+  const cudaError_t e = launch_rows(logprob_kernel<T, KV, NT, kCtas, kGrad>, a, a.rows, size, NT, stream);
   return e == cudaSuccess ? SEQSUM_OK : note_cuda(e);
 }
 
@@ -155,23 +189,23 @@ int run_logprob(const LogprobArgs &a, int size, cudaStream_t stream) {
 // the rows are few.
 template <typename T, bool kGrad>
 int choose_logprob(const LogprobArgs &a, cudaStream_t stream) {
-  constexpr int NT = 512;
-  const int64_t vecs = ((int64_t)a.vocab + 2 * Elem<T>::kPerVec - 2) / Elem<T>::kPerVec;   // whatever the alignment
+  const int64_t vecs = ((int64_t)a.vocab + Elem<T>::kPerVec - 1) / Elem<T>::kPerVec + 1;   // whatever the alignment
   const int sms = multiprocessors();
   int size = 1;
-  while (size < kMaxCluster && (vecs > (int64_t)size * NT * 8 || a.rows * size * 2 <= sms)) size *= 2;
-  const int64_t per = ((vecs + size - 1) / size + NT - 1) / NT;
-  if (per <= 1) return run_logprob<T, 1, NT, kGrad>(a, size, stream);
-  if (per <= 2) return run_logprob<T, 2, NT, kGrad>(a, size, stream);
-  if (per <= 4) return run_logprob<T, 4, NT, kGrad>(a, size, stream);
-  if (per <= 8) return run_logprob<T, 8, NT, kGrad>(a, size, stream);
-  return run_logprob<T, 0, NT, kGrad>(a, size, stream);
+  while (size < kMaxCluster && (vecs > (int64_t)size * 256 * 8 || a.rows * size * 2 <= sms)) size *= 2;
+  const int64_t mine = (vecs + size - 1) / size;
+  if (mine <= 256) return run_logprob<T, 1, 256, 8, kGrad>(a, size, stream);
+  if (mine <= 512) return run_logprob<T, 2, 256, 6, kGrad>(a, size, stream);
+  if (mine <= 1024) return run_logprob<T, 4, 256, 5, kGrad>(a, size, stream);
+  if (mine <= 2304) return run_logprob<T, 9, 256, 4, kGrad>(a, size, stream);
+  if (mine <= 4608) return run_logprob<T, 9, 512, 2, kGrad>(a, size, stream);
+  return run_logprob<T, 0, 512, 3, kGrad>(a, size, stream);
 }
 
 template <typename T>
 int run_backward(LogprobArgs &a, cudaStream_t stream) {
   constexpr int NT = 256, KV = 4;
-  const int64_t vecs = ((int64_t)a.vocab + 2 * Elem<T>::kPerVec - 2) / Elem<T>::kPerVec;
+  const int64_t vecs = ((int64_t)a.vocab + Elem<T>::kPerVec - 1) / Elem<T>::kPerVec + 1;
   a.parts = (int32_t)((vecs + NT * KV - 1) / (NT * KV));
   if (a.parts < 1) a.parts = 1;
   if (a.rows * a.parts > 0x7fffffff) return SEQSUM_EINVAL;

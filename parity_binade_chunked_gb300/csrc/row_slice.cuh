@@ -33,6 +33,11 @@ struct Elem<float> {
   __device__ static uint4 pack(const float *x) {
     return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
   }
+  // the maximum of a vector's numbers and m; NaN is passed over
+  __device__ static float vec_max(uint4 v, float m) {
+    const float a = fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), b = fmaxf(__uint_as_float(v.z), __uint_as_float(v.w));
+    return fmaxf(m, fmaxf(a, b));
+  }
   __device__ static float load(const float *p) { return *p; }
   __device__ static void store(float *p, float x) { *p = x; }
 };
@@ -53,6 +58,11 @@ struct Elem<__nv_bfloat16> {
       w[i] = *reinterpret_cast<const uint32_t *>(&b);
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ static float vec_max(uint4 v, float m) {
+    const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&v);
+    const __nv_bfloat162 a = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+    return fmaxf(m, fmaxf(__low2float(a), __high2float(a)));
   }
   __device__ static float load(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
   __device__ static void store(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
@@ -78,9 +88,33 @@ struct Elem<__half> {
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
+  __device__ static float vec_max(uint4 v, float m) {
+    const __half2 *h = reinterpret_cast<const __half2 *>(&v);
+    const __half2 a = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+    return fmaxf(m, fmaxf(__low2float(a), __high2float(a)));
+  }
   __device__ static float load(const __half *p) { return __half2float(*p); }
   __device__ static void store(__half *p, float x) { *p = __float2half_rn(x); }
 };
+
+// ---- two fp32 operations in one instruction, each rounded as by itself
+
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void split(uint64_t r, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r)); }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 
 // ---- clusters
 
@@ -205,6 +239,18 @@ struct Slice {
 #pragma unroll
       for (int k = 0; k < KV; k++) keep[k] = read(k);
     }
+  }
+  // the largest number of the slice; NaN is passed over
+  __device__ __forceinline__ float largest() const {
+    float m = -INFINITY;
+    if constexpr (KV > 0) {
+#pragma unroll
+      for (int k = 0; k < KV; k++)
+        if (k < steps) m = Elem<T>::vec_max(keep[k], m);
+    } else {
+      for (int k = 0; k < steps; k++) m = Elem<T>::vec_max(read(k), m);
+    }
+    return m;
   }
   // f(step, its elements as floats) for every step in index order
   template <typename F>
