@@ -176,6 +176,17 @@ __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
   return v;
 }
+__device__ __forceinline__ float warp_max_all(float v) {
+  // floats as unsigned integers of the same order
+  const uint32_t b = __float_as_uint(v), k = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+  const uint32_t m = __reduce_max_sync(~0u, k);
+  return __uint_as_float(m & 0x80000000u ? m ^ 0x80000000u : ~m);
+}
+__device__ __forceinline__ uint64_t warp_sum_62(uint64_t v) {   // of values below 2^62, sums too
+  const uint32_t lo = __reduce_add_sync(~0u, (uint32_t)v & 0xffffffu), mid = __reduce_add_sync(~0u, (uint32_t)(v >> 24) & 0xffffffu),
+                 hi = __reduce_add_sync(~0u, (uint32_t)(v >> 48));
+  return lo + ((uint64_t)mid << 24) + ((uint64_t)hi << 48);
+}
 __device__ __forceinline__ uint64_t warp_scan(uint64_t v, int lane) {   // inclusive
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -287,20 +298,193 @@ struct Slice {
   }
 };
 
+// ---- rows streamed through shared memory
+//
+// A cluster takes row after row.  Each of its CTAs copies its slice of a row
+// into one of two buffers in shared memory with one bulk copy, two rows ahead
+// of the row that is worked on; passes over a row read the buffer.
+//
+// A row's 16-byte vectors (as for Slice) are cut into blocks of 128; the CTAs
+// take consecutive runs of blocks, and a block belongs to one warp: lane l has
+// its vectors l, l + 32, l + 64, l + 96.  So whatever the cluster's size, the
+// same four vectors meet in one thread.
+//
+// Vectors that stick out of the row are put together by the lane that owns
+// them from elements read one by one; bulk copies stay inside the row.
+//
+// The cluster's warps tell each other 8-byte values through `Exchange`: every
+// warp writes to every CTA, the writes count down a barrier in each.  One
+// exchange of a row is done in every warp before any warp posts the exchange
+// after the next, so two of them in turn need one box each, and once a row's
+// first exchange is done all warps have left the row before: its buffer takes
+// the row after the next.
+
+constexpr uint64_t kWaitNs = 2000000000ull;   // waits for copies and for other CTAs give up after 2 s
+
+__device__ __forceinline__ uint32_t smem(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void bar_init(uint64_t *bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem(bar)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint64_t *bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem(bar)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint64_t *bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem(bar)), "r"(parity)
+      : "memory");
+  return done;
+}
+static __device__ __noinline__ bool bar_wait_long(uint64_t *bar, uint32_t parity) {
+  uint64_t t0, t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+  do {
+    for (int i = 0; i < 64; i++)
+      if (bar_try(bar, parity)) return true;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  } while (t - t0 < kWaitNs);
+  return false;
+}
+// false: gave up
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity) {
+  return bar_try(bar, parity) || bar_wait_long(bar, parity);
+}
+
+template <int NT>
+struct Exchange {
+  static constexpr int kWarps = NT / 32;
+  uint64_t box[kMaxCluster * kWarps];
+  uint64_t bar;
+
+  __device__ void init(uint32_t size) {   // one thread, before the cluster's first barrier
+    bar_init(&bar, 1);
+    bar_expect(&bar, size * kWarps * 8);
+  }
+  // v of every lane (the same) to every CTA
+  __device__ __forceinline__ void post(uint64_t v, uint32_t rank, uint32_t size) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (lane < (int)size)
+      asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.u64 [%0], %1, [%2];" ::"r"(
+                       remote(&box[rank * kWarps + warp], lane)),
+                   "l"(v), "r"(remote(&bar, lane))
+                   : "memory");
+  }
+  // waits for all warps' values; the thread that says so readies the barrier for the next time
+  __device__ __forceinline__ bool wait(uint32_t parity, uint32_t size) {
+    const bool ok = bar_wait(&bar, parity);
+    if (threadIdx.x == 0) bar_expect(&bar, size * kWarps * 8);
+    return ok;
+  }
+};
+
+// Where a row's slice of this CTA lies.
+template <typename T, int NT>
+struct Stream {
+  static constexpr int kE = Elem<T>::kPerVec;
+  static constexpr int kWarps = NT / 32;
+  const T *p;          // the row
+  int32_t vocab, off;
+  int32_t begin, n;    // this CTA's first vector, and how many it has
+  uint4 *buf;
+
+  __device__ __forceinline__ void set(const T *row, int32_t v, int32_t blocks, uint32_t rank, uint4 *b) {
+    p = row;
+    vocab = v;
+    off = (int32_t)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
+    const int32_t vecs = (off + v + kE - 1) / kE;
+    begin = min(blocks * 128 * (int32_t)rank, vecs);
+    n = min(blocks * 128, vecs - begin);
+    buf = b;
+  }
+  __device__ __forceinline__ bool cut_head() const { return off > 0 && begin == 0 && n > 0; }
+  __device__ __forceinline__ bool cut_tail() const { return n > 0 && (begin + n) * kE - off > vocab; }
+  // one thread: the copy of the vectors that lie inside the row
+  __device__ __forceinline__ void copy(uint64_t *full) const {
+    const int32_t from = cut_head() ? 1 : 0, to = n - (cut_tail() ? 1 : 0);
+    const uint32_t bytes = to > from ? (uint32_t)(to - from) * 16 : 0;
+    bar_expect(full, bytes);
+    if (bytes)
+      asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                       smem(buf + from)),
+                   "l"(p + (begin + from) * kE - off), "r"(bytes), "r"(smem(full))
+                   : "memory");
+  }
+  __device__ __forceinline__ bool owns(int32_t vec) const {
+    return (vec >> 7) % kWarps == (int32_t)(threadIdx.x >> 5) && (vec & 31) == (int32_t)(threadIdx.x & 31);
+  }
+  __device__ __forceinline__ uint4 by_elements(int32_t vec) const {
+    float x[kE];
+    const int32_t i = (begin + vec) * kE - off;
+#pragma unroll
+    for (int e = 0; e < kE; e++) x[e] = i + e >= 0 && i + e < vocab ? Elem<T>::load(p + i + e) : -INFINITY;
+    return Elem<T>::pack(x);
+  }
+  // the vectors that stick out, read by their owner into `head` and `tail` ...
+  __device__ __forceinline__ void read_edges(uint4 &head, uint4 &tail) const {
+    if (cut_head() && owns(0)) head = by_elements(0);
+    if (cut_tail() && owns(n - 1)) tail = by_elements(n - 1);
+  }
+  // ... and put into the buffer, where only the owner reads them
+  __device__ __forceinline__ void put_edges(uint4 head, uint4 tail) const {
+    const bool h = cut_head() && owns(0), t = cut_tail() && owns(n - 1);
+    if (h) buf[0] = head;
+    if (t) buf[n - 1] = tail;
+    if (h || t) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // a later copy may write these places
+  }
+  __device__ __forceinline__ int32_t index(int32_t vec, int e) const { return (begin + vec) * kE + e - off; }
+
+  // f(first vector's place, four vectors): this thread's share of each block;
+  // what is not in the row is -inf
+  template <typename F>
+  __device__ __forceinline__ void blocks(F f) const {
+    constexpr uint32_t ninf = Elem<T>::kNegInf;
+    const int lane = threadIdx.x & 31;
+    for (int32_t b = (int32_t)(threadIdx.x >> 5) * 128; b < n; b += kWarps * 128) {
+      uint4 v[4];
+      if (b + 128 <= n) {
+#pragma unroll
+        for (int s = 0; s < 4; s++) v[s] = buf[b + s * 32 + lane];
+      } else {
+#pragma unroll
+        for (int s = 0; s < 4; s++)
+          v[s] = b + s * 32 + lane < n ? buf[b + s * 32 + lane] : make_uint4(ninf, ninf, ninf, ninf);
+      }
+      f(b + lane, v);
+    }
+  }
+  // writes vector `vec` to the same place of another row
+  __device__ __forceinline__ void write(T *row, bool aligned, int32_t vec, const float *x) const {
+    if (vec >= n) return;
+    const int32_t i = (begin + vec) * kE - off;
+    if (aligned && i >= 0 && i + kE <= vocab) {
+      *reinterpret_cast<uint4 *>(row + i) = Elem<T>::pack(x);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kE; e++)
+        if (i + e >= 0 && i + e < vocab) Elem<T>::store(row + i + e, x[e]);
+    }
+  }
+};
+
 // A launch of `rows` clusters of `size` CTAs.
 template <typename Args>
 inline cudaError_t launch_rows(void (*kernel)(Args), const Args &args, int64_t rows, int size, int threads,
-                               cudaStream_t stream) {
+                               size_t shared, cudaStream_t stream, int *most = nullptr) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(rows * size));
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = shared;
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = size;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = size > 1 ? 1 : 0;
+  cfg.numAttrs = 1;
+  if (most) return cudaOccupancyMaxActiveClusters(most, (const void *)kernel, &cfg);
   return cudaLaunchKernelEx(&cfg, kernel, args);
 }
 

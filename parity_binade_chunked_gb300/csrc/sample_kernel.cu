@@ -335,7 +335,7 @@ __global__ __launch_bounds__(NT) void sample_kernel(const SampleArgs a) {
 
 template <typename T, int KV, int NT>
 int run_sample(const SampleArgs &a, int size, cudaStream_t stream) {
-  const cudaError_t e = launch_rows(sample_kernel<T, KV, NT>, a, a.rows, size, NT, stream);
+  const cudaError_t e = launch_rows(sample_kernel<T, KV, NT>, a, a.rows, size, NT, 0, stream);
   return e == cudaSuccess ? SEQSUM_OK : note_cuda(e);
 }
 
