@@ -4,10 +4,11 @@
 //   lse = m + ln sum exp(x_i - m),  logp = x_t - lse,
 //   d logits_i = dlogp * ([i = t] - exp(x_i - lse))
 //
-// The exponentials of a 16-byte vector are added in fp32, the vectors' sums
-// as integers (2^-38 a unit): the row's sum does not depend on how it is
-// split over threads and CTAs, so a row's results do not depend on the other
-// rows of the call.
+// A row is cut into segments by its length alone, one for each warp that works
+// on it.  A segment's maximum and the
+// sum of its exponentials relative to that are formed by one warp in one
+// order, and the segments' sums are joined in one order: a row's results do
+// not depend on how many CTAs share it, so not on the other rows of the call.
 #include <math.h>
 
 #include <atomic>
@@ -21,8 +22,6 @@ namespace {
 using namespace row;
 
 constexpr float kLog2e = 1.44269504f;
-constexpr float kUnit = 274877906944.0f;             // 2^38: at most 2^22 vectors of at most 4, or 2^21 of 8
-constexpr uint64_t kBad = 1ull << 63;                // marks a sum with something in it that is no number
 
 struct LogprobArgs {
   const void *logits;
@@ -34,7 +33,7 @@ struct LogprobArgs {
   void *dlogits;
   int64_t dstride;
   int32_t parts;                                     // backward: CTAs a row
-  int32_t blocks;                                    // blocks of 128 vectors a CTA takes of a row
+  int32_t steps;                                     // that a CTA takes of a row at most
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -74,33 +73,65 @@ __device__ __forceinline__ float vec_sum(uint4 w, float base) {
   return p + q;
 }
 
-// x, at most 32, in units of 2^-38: two halves, each rounded to an integer by
-// adding a number whose last place is 1 (a conversion to 64 bits goes through
-// the fp64 pipe, of which this GPU has little).
-__device__ __forceinline__ uint64_t fixed38(float x) {
-  const float big = x * 131072.0f, h = big + 8388608.0f, rest = __fmaf_rn(x, 131072.0f, -(h - 8388608.0f));
-  const float l = __fmaf_rn(rest, 2097152.0f, 12582912.0f);
-  return (uint64_t)((int64_t)(__float_as_int(h) - 0x4b000000) * 2097152 + (__float_as_int(l) - 0x4b400000));
+// A thread's part of a segment: the largest number so far and the sum of
+// exp(x - largest), four vectors at a time.  While all is -inf the sum is 0
+// (with NaN beside it: the largest is -inf, but the sum is NaN).
+struct Part {
+  float m = -INFINITY, s = 0.0f;
+  template <typename T, int N>
+  __device__ __forceinline__ void add(const uint4 *v) {
+    float to = m;
+#pragma unroll
+    for (int k = 0; k < N; k++) to = Elem<T>::vec_max(v[k], to);
+    const float base = to == -INFINITY ? 0.0f : to;
+    float t[N];
+#pragma unroll
+    for (int k = 0; k < N; k++) t[k] = vec_sum<T>(v[k], base);
+#pragma unroll
+    for (int o = N / 2; o; o >>= 1)
+#pragma unroll
+      for (int k = 0; k < o; k++) t[k] += t[k + o];
+    s = s * ex2((m - base) * kLog2e) + t[0];
+    m = to;
+  }
+  // the warp's, as (largest, sum)
+  __device__ __forceinline__ uint64_t of_warp() const {
+    const float to = warp_max_all(m), base = to == -INFINITY ? 0.0f : to;
+    return pair(to, warp_add(s * ex2((m - base) * kLog2e)));
+  }
+};
+
+// The largest number and the sum of several (at most 64) parts, in every
+// thread: lane l joins parts l and l + 32, then the lanes.
+__device__ __forceinline__ void join(const uint64_t *box, int n, float &m, float &sum) {
+  const int lane = threadIdx.x & 31;
+  float m0 = -INFINITY, s0 = 0.0f, m1 = -INFINITY, s1 = 0.0f;
+  if (lane < n) split(box[lane], m0, s0);
+  if (lane + 32 < n) split(box[lane + 32], m1, s1);
+  m = warp_max_all(fmaxf(m0, m1));
+  const float base = m == -INFINITY ? 0.0f : m;
+  sum = warp_add(s0 * ex2((m0 - base) * kLog2e) + s1 * ex2((m1 - base) * kLog2e));
 }
 
-// Writes a vector's gradient: coef * exponential, and `g` more at the token.
-template <typename T, typename S>
-__device__ __forceinline__ void vec_gradient(const S &x, int32_t vec, uint4 w, float base, T *d, bool aligned, float coef,
-                                             float g, int32_t token) {
+// exp(x - base) * coef of a vector
+template <typename T>
+__device__ __forceinline__ void vec_scaled(uint4 w, float base, float coef, float *y) {
   constexpr int kE = Elem<T>::kPerVec;
-  float v[kE], y[kE];
+  float v[kE];
   Elem<T>::unpack(w, v);
   exps<kE>(v, base, y);
   const uint64_t c = pair(coef, coef);
 #pragma unroll
   for (int e = 0; e < kE; e += 2) split(mul2(pair(y[e], y[e + 1]), c), y[e], y[e + 1]);
-  const int32_t at = token - x.index(vec, 0);
-  if (at >= 0 && at < kE) {
+}
+// `g` more where `at`, the token's place from the vector's start, is in it
+template <int kE>
+__device__ __forceinline__ void vec_token(int32_t at, float g, float *y) {
+  if ((uint32_t)at < (uint32_t)kE) {
 #pragma unroll
     for (int e = 0; e < kE; e++)
       if (e == at) y[e] += g;
   }
-  x.write(d, aligned, vec, y);
 }
 
 template <typename S, typename T>
@@ -114,144 +145,203 @@ __device__ __forceinline__ bool same_alignment(const T *d, int32_t off) {
   return (reinterpret_cast<uintptr_t>(d) & 15) / sizeof(T) == (uintptr_t)off;
 }
 
-template <int NT>
-struct LogprobShared {
-  Exchange<NT> top, sum;
-  uint64_t full[2];
-};
+constexpr int kBoxes = 4;   // exchanges under way, a power of two
 
-// A cluster's rows one after another (see Stream): the maximum, the sum, the
-// gradient, each a pass over the row's buffer.
-template <typename T, int NT, bool kGrad>
-__global__ __launch_bounds__(NT) void logprob_kernel(const LogprobArgs a) {
-  extern __shared__ uint4 buffers[];
-  __shared__ LogprobShared<NT> sh;
-  constexpr int kE = Elem<T>::kPerVec, kBoxes = kMaxCluster * (NT / 32);
+// Rows on chip in a CTA: one coming, one at work; and one more where a row's
+// gradient waits while the next row is summed.
+constexpr int kWarps = 8, kLog2Warps = 3;   // and the producer
+template <bool kGrad>
+constexpr int kBuffers = 2;
+template <bool kGrad>
+constexpr int kLag = kGrad ? 0 : 1;   // whether the next row is summed before a row is finished
+
+// A cluster's rows one after another (see Stream): a row's segments, and the
+// sum and gradient of that row or the one before.
+template <typename T, bool kGrad>
+__global__ __launch_bounds__(kWarps * 32 + 32) void logprob_kernel(const LogprobArgs a) {
+  extern __shared__ uint4 buffers[];   // kB buffers of a.steps steps
+  constexpr int kE = Elem<T>::kPerVec, kB = kBuffers<kGrad>, kL = kLag<kGrad>;
+  __shared__ uint64_t full[kB], empty[kB], told[kBoxes], box[kBoxes][kMaxCluster * kWarps];
   const uint32_t size = cluster_size(), rank = cluster_rank();
-  const int lane = threadIdx.x & 31;
-  const int64_t first = blockIdx.x / size, step = gridDim.x / size;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t first = blockIdx.x / size, step = gridDim.x / size;
+  const uint32_t turns = ((uint32_t)a.rows - first + step - 1) / step;   // (at most one cluster a row)
+  const int log2_size = __ffs(size) - 1, log2_segments = log2_size + kLog2Warps, segments = (int)size * kWarps;
   if (threadIdx.x == 0) {
-    sh.top.init(size);
-    sh.sum.init(size);
-    bar_init(&sh.full[0], 1);
-    bar_init(&sh.full[1], 1);
+    for (int b = 0; b < kB; b++) bar_init(&full[b], 2), bar_init(&empty[b], kWarps);
+    for (int b = 0; b < kBoxes; b++) {
+      bar_init(&told[b], 1);
+      bar_expect(&told[b], segments * 8);
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  auto stream = [&](int64_t row, int b) {
-    Stream<T, NT> x;
-    x.set(static_cast<const T *>(a.logits) + row * a.stride, a.vocab, a.blocks, rank, buffers + b * a.blocks * 128);
-    return x;
-  };
-  uint4 head, tail;
-  if (threadIdx.x == 0) {
-    stream(first, 0).copy(&sh.full[0]);
-    if (first + step < a.rows) stream(first + step, 1).copy(&sh.full[1]);
-  }
-  stream(first, 0).read_edges(head, tail);
   cluster_sync();   // every CTA's barriers are ready
 
+  auto row_of = [&](uint32_t it) { return (int64_t)(first + it * step); };
+  auto stream = [&](uint32_t it, uint32_t b) {
+    Stream<T> x;
+    x.set(static_cast<const T *>(a.logits) + row_of(it) * a.stride, a.vocab, rank, log2_size, buffers + b * a.steps * 32);
+    return x;
+  };
   bool ok = true;
-  uint32_t it = 0;
-  for (int64_t row = first; row < a.rows && ok; row += step, it++) {
-    const Stream<T, NT> x = stream(row, it & 1);
-    const int64_t token = a.tokens[row];
-    const bool used = token >= 0 && token < a.vocab;
-    const float dlogp = kGrad ? a.dlogps[row] : 0.0f;
-    x.put_edges(head, tail);
-    if (row + step < a.rows) stream(row + step, 0).read_edges(head, tail);
-    ok &= bar_wait(&sh.full[it & 1], (it >> 1) & 1);
-
-    float m = -INFINITY;
-    x.blocks([&](int32_t, const uint4 *v) {
-#pragma unroll
-      for (int s = 0; s < 4; s++) m = Elem<T>::vec_max(v[s], m);
-    });
-    sh.top.post(__float_as_uint(warp_max_all(m)), rank, size);
-    ok &= sh.top.wait(it & 1, size);
-    // every warp has left the row before: its buffer is free
-    if (threadIdx.x == 0 && it > 0 && row + step < a.rows) stream(row + step, (it + 1) & 1).copy(&sh.full[(it + 1) & 1]);
-    m = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < kBoxes; i += 32)
-      if (i + lane < (int)size * (NT / 32)) m = fmaxf(m, __uint_as_float((uint32_t)sh.top.box[i + lane]));
-    m = warp_max_all(m);
-    // a row of nothing but -inf: every exponential is 0 (with NaN beside them: m is -inf, but the sum is NaN)
-    const float base = m == -INFINITY ? 0.0f : m;
-
-    uint64_t sum = 0;
-    float check = 0.0f;
-    x.blocks([&](int32_t, const uint4 *v) {
-      float t[4];
-#pragma unroll
-      for (int s = 0; s < 4; s++) t[s] = vec_sum<T>(v[s], base);
-      const float q = (t[0] + t[1]) + (t[2] + t[3]);
-      check += q;
-      sum += fixed38(q);
-    });
-    const bool none = __any_sync(~0u, !(check < INFINITY));   // some exponential is no number
-    sh.sum.post(none ? kBad : warp_sum_62(sum), rank, size);
-    ok &= sh.sum.wait(it & 1, size);
-    bool bad = false;
-    sum = 0;
-#pragma unroll
-    for (int i = 0; i < kBoxes; i += 32)
-      if (i + lane < (int)size * (NT / 32)) {
-        const uint64_t v = sh.sum.box[i + lane];
-        bad |= (v & kBad) != 0;
-        sum += v & ~kBad;
-      }
-    bad = __any_sync(~0u, bad) || !ok;
-    sum = warp_sum_62(sum);
-    const float s = bad ? NAN : (float)sum * (1.0f / kUnit);
-    const bool nothing = m == -INFINITY && !bad;
-    const float ln = logf(s);
-    if (rank == 0 && threadIdx.x == 0) {
-      a.lses[row] = base + ln;
-      if (!used) a.logps[row] = 0.0f;
+  if (warp == kWarps) {
+    for (uint32_t it = 0, b = 0, use = 0; it < turns; it++) {
+      if (use > 0) ok = __all_sync(~0u, bar_wait(&empty[b], (use - 1) & 1));
+      if (!ok) break;
+      stream(it, b).bring(static_cast<const T *>(a.logits) + row_of(it) * a.stride, &full[b]);
+      if (++b == kB) b = 0, use++;
     }
-    const int32_t vec = (int32_t)(token + x.off) / kE - x.begin;   // the token's
-    if (used && vec >= 0 && vec < x.n && x.owns(vec)) {
-      float v[kE], xt = 0.0f;
-      Elem<T>::unpack(x.buf[vec], v);
-#pragma unroll
-      for (int e = 0; e < kE; e++)
-        if (x.index(vec, e) == token) xt = v[e];
-      a.logps[row] = nothing ? -INFINITY : (xt - base) - ln;
-    }
-    if constexpr (kGrad) {
-      T *d = static_cast<T *>(a.dlogits) + row * a.dstride;
-      const bool aligned = same_alignment(d, x.off);
-      const float coef = -__fdiv_rn(dlogp, s);
-      const bool zero = !used || nothing;
-      x.blocks([&](int32_t vec, const uint4 *v) {
-#pragma unroll
-        for (int s = 0; s < 4; s++) {
-          if (zero) {
-            const float y[kE] = {};
-            x.write(d, aligned, vec + 32 * s, y);
-          } else {
-            vec_gradient<T>(x, vec + 32 * s, v[s], base, d, aligned, coef, dlogp, (int32_t)token);
-          }
+  } else {
+    const uint32_t segment = rank * kWarps + warp;
+    Stream<T> was;
+    int64_t was_token = 0;
+    float was_xt = 0.0f, was_dlogp = 0.0f;   // the logit of the token, in the thread that has it
+    bool was_mine = false;
+    uint32_t was_b = 0;
+    for (uint32_t it = 0, b = 0, parity = 0; it < turns + kL && ok; it++) {
+      Stream<T> x;
+      int64_t token = 0;
+      float xt = 0.0f, dlogp = 0.0f;
+      bool have = false;
+      if (!kL || it < turns) {
+        x = stream(it, b);
+        token = a.tokens[row_of(it)];
+        if (kGrad) dlogp = a.dlogps[row_of(it)];
+        ok &= bar_wait(&full[b], parity);
+        const Exchange tell = {box[it % kBoxes], &told[it % kBoxes], (uint32_t)segments * 8};
+        int32_t st = x.step_of(segment, log2_segments) - x.begin / 32;
+        const int32_t end = x.step_of(segment + 1, log2_segments) - x.begin / 32;
+        Part part;
+        const uint4 *p = x.buf + st * 32 + lane;
+        for (; st + 4 <= end; st += 4, p += 128) {
+          const uint4 v[4] = {p[0], p[32], p[64], p[96]};
+          part.add<T, 4>(v);
         }
-      });
+        if (st + 2 <= end) {
+          const uint4 v[2] = {p[0], p[32]};
+          part.add<T, 2>(v);
+          st += 2, p += 64;
+        }
+        if (st < end) part.add<T, 1>(p);
+        tell.post(segment, part.of_warp(), size);
+        const int32_t vec = (int32_t)(token + x.off) / kE - x.begin;   // the token's
+        if (token >= 0 && token < a.vocab && vec >= 0 && vec < x.n && (int)threadIdx.x == vec % (kWarps * 32)) {
+          xt = Elem<T>::load(reinterpret_cast<const T *>(x.buf + vec) + (token - x.index(vec, 0)));
+          have = true;
+        }
+        if (!kGrad) {
+          __syncwarp();
+          if (lane == 0) bar_arrive(&empty[b]);
+        }
+      }
+      if (!kL) was = x, was_token = token, was_xt = xt, was_dlogp = dlogp, was_mine = have, was_b = b;
+      if (it >= kL) {
+        const int64_t row = row_of(it - kL);
+        const uint32_t t = (it - kL) % kBoxes;
+        ok &= bar_wait(&told[t], ((it - kL) / kBoxes) & 1);
+        if (threadIdx.x == 0) bar_expect(&told[t], segments * 8);   // for its next row
+        float m, s;
+        join(box[t], segments, m, s);
+        const float base = m == -INFINITY ? 0.0f : m;
+        if (!__all_sync(~0u, ok)) s = NAN;   // a wait gave up
+        const bool used = was_token >= 0 && was_token < a.vocab, nothing = s == 0.0f;
+        if (rank == 0 && threadIdx.x == 0) {
+          a.lses[row] = base + logf(s);
+          if (!used) a.logps[row] = 0.0f;
+        }
+        if (was_mine) a.logps[row] = nothing ? -INFINITY : (was_xt - base) - logf(s);
+        if constexpr (kGrad) {
+          T *d = static_cast<T *>(a.dlogits) + row * a.dstride;
+          const bool aligned = same_alignment(d, was.off);
+          const float coef = -__fdiv_rn(was_dlogp, s);
+          const bool zero = !used || nothing;
+          const int32_t begin = was.step_of(segment, log2_segments) - was.begin / 32,
+                        end = was.step_of(segment + 1, log2_segments) - was.begin / 32;
+#pragma unroll 4
+          for (int32_t st = begin; st < end; st++) {
+            const int32_t vec = st * 32 + lane, at = was.index(vec, 0);
+            float y[kE];
+            if (zero) {
+#pragma unroll
+              for (int e = 0; e < kE; e++) y[e] = 0.0f;
+            } else {
+              vec_scaled<T>(was.buf[vec], base, coef, y);
+              vec_token<kE>((int32_t)was_token - at, was_dlogp, y);
+            }
+            if (aligned && was.inside(st)) *reinterpret_cast<uint4 *>(d + at) = Elem<T>::pack(y);
+            else was.write_edge(d, vec, y);
+          }
+          __syncwarp();
+          if (lane == 0) bar_arrive(&empty[was_b]);
+        }
+      }
+      if (kL) was = x, was_token = token, was_xt = xt, was_dlogp = dlogp, was_mine = have, was_b = b;
+      if (++b == kB) b = 0, parity ^= 1;
+      ok = __all_sync(~0u, ok);
+      if (!ok && rank == 0 && lane == 0)   // what is not done is marked
+        for (uint32_t i = it >= kL ? it - kL : 0; i < turns; i++) a.lses[row_of(i)] = a.logps[row_of(i)] = NAN;
     }
-    ok = __all_sync(~0u, ok);
+    // copies in flight land before the CTA goes (in a call that went well none are)
+    if (!ok)
+      for (int b = 0; b < kB; b++)
+        for (uint32_t parity = 0; parity < 2; parity++) bar_wait(&full[b], parity);
   }
-  if (!ok) {
-    // a wait gave up: what is not done is marked, copies in flight may land before the CTA goes
-    for (int64_t row = first; row < a.rows; row += step)
-      if (rank == 0 && threadIdx.x == 0 && (row - first) / step >= (int64_t)it - 1) a.lses[row] = a.logps[row] = NAN;
-    bar_wait(&sh.full[it & 1], (it >> 1) & 1);
-    bar_wait(&sh.full[(it - 1) & 1], ((it - 1) >> 1) & 1);
-  }
+  __syncwarp();
   cluster_sync();
+}
+
+// Short rows: a warp each, in registers.  (8192 x 3001 bf16 rows, gradient:
+// 29 us, the host's time; 46 us streamed.  4090: 49 and 51.)
+template <typename T, int KV, bool kGrad>
+__global__ __launch_bounds__(128) void logprob_short_kernel(const LogprobArgs a) {
+  constexpr int kE = Elem<T>::kPerVec;
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (row >= a.rows) return;
+  const int lane = threadIdx.x & 31;
+  const T *p = static_cast<const T *>(a.logits) + row * a.stride;
+  Slice<T, KV, 32> x;
+  x.set(p, a.vocab, 0, 1);
+  x.load();
+  const int64_t token = a.tokens[row];
+  const bool used = token >= 0 && token < a.vocab;
+  const float xt = used ? Elem<T>::load(p + token) : 0.0f;   // before a gradient in place overwrites it
+  Part part;
+#pragma unroll
+  for (int k = 0; k < KV; k += 4)
+    if (k < x.steps) part.add<T, 4>(x.keep + k);
+  float m, s;
+  split(part.of_warp(), m, s);
+  const float base = m == -INFINITY ? 0.0f : m;
+  const bool nothing = s == 0.0f;
+  if (lane == 0) {
+    const float ln = logf(s);
+    a.lses[row] = base + ln;
+    a.logps[row] = used ? (nothing ? -INFINITY : (xt - base) - ln) : 0.0f;
+  }
+  if constexpr (kGrad) {
+    T *d = static_cast<T *>(a.dlogits) + row * a.dstride;
+    const bool aligned = same_alignment(d, x.off);
+    if (!used || nothing) {
+      write_zeros(x, d, aligned);
+    } else {
+      const float dlogp = a.dlogps[row], coef = -__fdiv_rn(dlogp, s);
+#pragma unroll
+      for (int k = 0; k < KV; k++)
+        if (k < x.steps) {
+          float y[kE];
+          vec_scaled<T>(x.keep[k], base, coef, y);
+          vec_token<kE>((int32_t)token - x.index(k, 0), dlogp, y);
+          x.write(d, aligned, k, y);
+        }
+    }
+  }
 }
 
 // Rows too large for the buffers: one CTA a part of a row, its passes read
 // global memory (L2).
 template <typename T, int NT, bool kGrad>
 __global__ __launch_bounds__(NT) void logprob_reread_kernel(const LogprobArgs a) {
-  __shared__ uint64_t box[2][kMaxCluster];
+  __shared__ uint64_t box[kMaxCluster];
   __shared__ uint64_t part[NT / 32];
   const uint32_t size = cluster_size(), rank = cluster_rank();
   const int64_t row = blockIdx.x / size;
@@ -264,35 +354,20 @@ __global__ __launch_bounds__(NT) void logprob_reread_kernel(const LogprobArgs a)
   const float xt = used ? Elem<T>::load(p + token) : 0.0f;   // before a gradient in place overwrites it
   const float dlogp = kGrad ? a.dlogps[row] : 0.0f;
 
-  float m = warp_max_all(x.largest());
-  if (lane == 0) part[warp] = __float_as_uint(m);
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < NT / 32; i++) m = fmaxf(m, __uint_as_float((uint32_t)part[i]));
-  cluster_post(__float_as_uint(m), box[0], rank, size);
-  for (uint32_t r = 0; r < size; r++) m = fmaxf(m, __uint_as_float((uint32_t)box[0][r]));
-  const float base = m == -INFINITY ? 0.0f : m;
-
-  uint64_t sum = 0;
-  float check = 0.0f;
-  for (int k = 0; k < x.steps; k++) {
-    const float q = vec_sum<T>(x.read(k), base);
-    check += q;
-    sum += fixed38(q);
+  Part mine;
+  for (int k = 0; k < x.steps; k += 4) {
+    const uint4 v[4] = {x.read(k), x.read(k + 1), x.read(k + 2), x.read(k + 3)};
+    mine.add<T, 4>(v);
   }
-  const bool bad = __any_sync(~0u, !(check < INFINITY));
-  sum = warp_sum_62(sum);
+  const uint64_t of_warp = mine.of_warp();
+  if (lane == 0) part[warp] = of_warp;
   __syncthreads();
-  if (lane == 0) part[warp] = bad ? kBad : sum;
-  __syncthreads();
-  uint64_t all = 0, flag = 0;
-#pragma unroll
-  for (int i = 0; i < NT / 32; i++) all += part[i] & ~kBad, flag |= part[i] & kBad;
-  cluster_post(all | flag, box[1], rank, size);   // no CTA reads or writes another's memory after this
-  all = flag = 0;
-  for (uint32_t r = 0; r < size; r++) all += box[1][r] & ~kBad, flag |= box[1][r] & kBad;
-  const float s = flag ? NAN : (float)all * (1.0f / kUnit);
-  const bool nothing = m == -INFINITY && !flag;
+  float m, s;
+  join(part, NT / 32, m, s);
+  cluster_post(pair(m, s), box, rank, size);   // no CTA reads or writes another's memory after this
+  join(box, (int32_t)size, m, s);
+  const float base = m == -INFINITY ? 0.0f : m;
+  const bool nothing = s == 0.0f;
   if (rank == 0 && threadIdx.x == 0) {
     const float ln = logf(s);
     a.lses[row] = base + ln;
@@ -305,7 +380,12 @@ __global__ __launch_bounds__(NT) void logprob_reread_kernel(const LogprobArgs a)
     if (!used || nothing) {
       write_zeros(x, d, aligned);
     } else {
-      for (int k = 0; k < x.steps; k++) vec_gradient<T>(x, k, x.read(k), base, d, aligned, coef, dlogp, (int32_t)token);
+      for (int k = 0; k < x.steps; k++) {
+        float y[x.kE];
+        vec_scaled<T>(x.read(k), base, coef, y);
+        vec_token<x.kE>((int32_t)token - x.index(k, 0), dlogp, y);
+        x.write(d, aligned, k, y);
+      }
     }
   }
 }
@@ -327,42 +407,64 @@ __global__ __launch_bounds__(NT) void backward_kernel(const LogprobArgs a) {
   } else {
 #pragma unroll
     for (int k = 0; k < KV; k++)
-      if (k < x.steps) vec_gradient<T>(x, k, x.keep[k], lse, d, aligned, -g, g, (int32_t)token);
+      if (k < x.steps) {
+        float y[x.kE];
+        vec_scaled<T>(x.keep[k], lse, -g, y);
+        vec_token<x.kE>((int32_t)token - x.index(k, 0), g, y);
+        x.write(d, aligned, k, y);
+      }
   }
 }
 
-constexpr int kThreads = 256;
-constexpr int kDevices = 16;                           // whose occupancy is kept
-constexpr int kMostBlocks = 54;                        // two buffers of 108 KB
+constexpr int kDevices = 16;           // whose occupancy is kept
+constexpr int kShort = 12;             // steps of the rows that a warp takes by itself
 
-// CTAs a row, and how many such clusters run at once.  Three CTAs with two
-// buffers of 32 KB keep an SM's share of copies in flight while others
-// compute; where the rows are few, more and smaller CTAs shorten each row.
+template <bool kGrad>
+constexpr size_t shared_bytes(int64_t steps) {
+  return (size_t)steps * kBuffers<kGrad> * 32 * 16;
+}
+// steps of a row that a CTA has room for
+template <bool kGrad>
+constexpr int kMostSteps = (224 << 10) / (kBuffers<kGrad> * 32 * 16);
+
+// CTAs a row, and how many such clusters run at once.  Two buffers of up to 52
+// KB let two CTAs share an SM (three up to 37 KB), so that some compute while
+// copies for others are in flight; fewer CTAs a row are better than more.
+// (8192 x 131072 bf16, gradient: 64 steps a CTA 695 us, 128 steps 957; 4000 x
+// 50000: 98 steps 133 us, 49 steps 155.)
 template <typename T, bool kGrad>
 int choose_logprob(LogprobArgs a, cudaStream_t stream) {
-  static std::atomic<int> fits[kDevices][4][kMostBlocks + 1];   // clusters at once, by their size and blocks (0: not known)
-  const int64_t vecs = ((int64_t)a.vocab + Elem<T>::kPerVec - 1) / Elem<T>::kPerVec + 1;   // whatever the alignment
-  const int64_t blocks = (vecs + 127) / 128;
-  const int sms = multiprocessors();
-  int size = 1, log2 = 0;
-  while (size < kMaxCluster && (blocks > (int64_t)size * 16 || a.rows * size * 2 <= sms)) size *= 2, log2++;
-  a.blocks = (int32_t)((blocks + size - 1) / size);
-  cudaError_t e;
-  if (a.blocks > kMostBlocks) {
-    e = launch_rows(logprob_reread_kernel<T, 512, kGrad>, a, a.rows, size, 512, 0, stream);
+  static std::atomic<int> fits[kDevices][4][kMostSteps<kGrad> + 1];   // clusters at once, by size and steps (0: not known)
+  constexpr int kE = Elem<T>::kPerVec;
+  const int64_t vecs = ((int64_t)a.vocab + kE - 1) / kE + 1;   // whatever the alignment
+  const int64_t steps = (vecs + 31) / 32;
+  if (steps <= kShort) {
+    const int64_t ctas = (a.rows + 3) / 4;
+    const cudaError_t e = steps <= 4   ? launch_rows(logprob_short_kernel<T, 4, kGrad>, a, ctas, 1, 128, 0, stream)
+                          : steps <= 8 ? launch_rows(logprob_short_kernel<T, 8, kGrad>, a, ctas, 1, 128, 0, stream)
+                                       : launch_rows(logprob_short_kernel<T, kShort, kGrad>, a, ctas, 1, 128, 0, stream);
     return e == cudaSuccess ? SEQSUM_OK : note_cuda(e);
   }
-  auto kernel = logprob_kernel<T, kThreads, kGrad>;
-  const size_t shared = (size_t)a.blocks * 2 * 128 * 16;
+  int size = 1, log2 = 0;
+  while (size < kMaxCluster && steps > (int64_t)size * 104) size *= 2, log2++;
+  a.steps = (int32_t)((steps + size - 1) / size);
+  cudaError_t e;
+  if (a.steps > kMostSteps<kGrad>) {
+    e = launch_rows(logprob_reread_kernel<T, 512, kGrad>, a, a.rows, kMaxCluster, 512, 0, stream);
+    return e == cudaSuccess ? SEQSUM_OK : note_cuda(e);
+  }
+  auto kernel = logprob_kernel<T, kGrad>;
+  constexpr int kThreads = kWarps * 32 + 32;
+  const size_t shared = shared_bytes<kGrad>(a.steps);
   int device = 0, most = 0;
   if ((e = cudaGetDevice(&device)) != cudaSuccess) return note_cuda(e);
-  if (device < kDevices) most = fits[device][log2][a.blocks].load(std::memory_order_relaxed);
+  if (device < kDevices) most = fits[device][log2][a.steps].load(std::memory_order_relaxed);
   if (most == 0) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostBlocks * 2 * 128 * 16);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared_bytes<kGrad>(kMostSteps<kGrad>));
     if (e == cudaSuccess) e = launch_rows(kernel, a, 1, size, kThreads, shared, stream, &most);
     if (e != cudaSuccess) return note_cuda(e);
     if (most < 1) return SEQSUM_ECUDA;
-    if (device < kDevices) fits[device][log2][a.blocks].store(most, std::memory_order_relaxed);
+    if (device < kDevices) fits[device][log2][a.steps].store(most, std::memory_order_relaxed);
   }
   e = launch_rows(kernel, a, a.rows < most ? a.rows : most, size, kThreads, shared, stream);
   return e == cudaSuccess ? SEQSUM_OK : note_cuda(e);

@@ -182,10 +182,10 @@ __device__ __forceinline__ float warp_max_all(float v) {
   const uint32_t m = __reduce_max_sync(~0u, k);
   return __uint_as_float(m & 0x80000000u ? m ^ 0x80000000u : ~m);
 }
-__device__ __forceinline__ uint64_t warp_sum_62(uint64_t v) {   // of values below 2^62, sums too
-  const uint32_t lo = __reduce_add_sync(~0u, (uint32_t)v & 0xffffffu), mid = __reduce_add_sync(~0u, (uint32_t)(v >> 24) & 0xffffffu),
-                 hi = __reduce_add_sync(~0u, (uint32_t)(v >> 48));
-  return lo + ((uint64_t)mid << 24) + ((uint64_t)hi << 48);
+__device__ __forceinline__ float warp_add(float v) {   // the same tree in every lane
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+  return v;
 }
 __device__ __forceinline__ uint64_t warp_scan(uint64_t v, int lane) {   // inclusive
 #pragma unroll
@@ -207,7 +207,8 @@ __device__ __forceinline__ uint64_t warp_scan(uint64_t v, int lane) {   // inclu
 // the row is touched; what is not in the row is -inf.
 //
 // KV > 0: at most KV steps, kept in registers.  KV = 0: any number of steps,
-// read again from global memory (L2) by every pass.
+// read again from global memory (L2) by every pass.  NT = 32: every warp has a
+// row of its own.
 template <typename T, int KV, int NT>
 struct Slice {
   static constexpr int kE = Elem<T>::kPerVec;
@@ -225,7 +226,7 @@ struct Slice {
     steps = (mine + NT - 1) / NT;
     const int32_t begin = mine * (int32_t)rank;
     limit = min(begin + mine, vecs);
-    first = begin + (int32_t)(threadIdx.x >> 5) * steps * 32 + (int32_t)(threadIdx.x & 31);
+    first = begin + (NT == 32 ? 0 : (int32_t)(threadIdx.x >> 5) * steps * 32) + (int32_t)(threadIdx.x & 31);
   }
   __device__ __forceinline__ int32_t index(int k, int e) const { return (first + 32 * k) * kE + e - off; }
   __device__ __forceinline__ uint4 read(int k) const {
@@ -300,30 +301,35 @@ struct Slice {
 
 // ---- rows streamed through shared memory
 //
-// A cluster takes row after row.  Each of its CTAs copies its slice of a row
-// into one of two buffers in shared memory with one bulk copy, two rows ahead
-// of the row that is worked on; passes over a row read the buffer.
+// A cluster takes row after row.  In each of its CTAs one warp (the producer)
+// brings the CTA's slice of each row into the next of a few buffers in shared
+// memory; the other warps make passes over the buffers and leave them one by
+// one.
 //
-// A row's 16-byte vectors (as for Slice) are cut into blocks of 128; the CTAs
-// take consecutive runs of blocks, and a block belongs to one warp: lane l has
-// its vectors l, l + 32, l + 64, l + 96.  So whatever the cluster's size, the
-// same four vectors meet in one thread.
+// A row's 16-byte vectors, counted from the aligned address at or below its
+// first element, go to the lanes of a warp in steps of 32, and the steps are
+// cut into segments as even as can be, one for each warp of the cluster.  The
+// cluster's size goes by the row's length alone, so the same vectors meet in
+// one thread in the same order whatever else a call holds.
 //
-// Vectors that stick out of the row are put together by the lane that owns
-// them from elements read one by one; bulk copies stay inside the row.
+// What lies inside the row comes by one bulk copy; vectors that stick out of
+// it are put together from elements read one by one, with -inf beside them and
+// after them up to the end of the last step.
 //
-// The cluster's warps tell each other 8-byte values through `Exchange`: every
-// warp writes to every CTA, the writes count down a barrier in each.  One
-// exchange of a row is done in every warp before any warp posts the exchange
-// after the next, so two of them in turn need one box each, and once a row's
-// first exchange is done all warps have left the row before: its buffer takes
-// the row after the next.
+// The CTAs tell each other 8 bytes a segment through `Exchange`: each is
+// written to every CTA, the writes count down a barrier there.  A warp may
+// post a row's segments before it waits for the row before; a post then comes
+// after every warp has left the exchange three rows before, so there are four
+// boxes in turn.
 
 constexpr uint64_t kWaitNs = 2000000000ull;   // waits for copies and for other CTAs give up after 2 s
 
 __device__ __forceinline__ uint32_t smem(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void bar_init(uint64_t *bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem(bar)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint64_t *bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem(bar)) : "memory");
 }
 __device__ __forceinline__ void bar_expect(uint64_t *bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem(bar)), "r"(bytes) : "memory");
@@ -353,119 +359,86 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity) {
   return bar_try(bar, parity) || bar_wait_long(bar, parity);
 }
 
-template <int NT>
 struct Exchange {
-  static constexpr int kWarps = NT / 32;
-  uint64_t box[kMaxCluster * kWarps];
-  uint64_t bar;
+  uint64_t *box;   // one for each segment of the row
+  uint64_t *bar;
+  uint32_t bytes;
 
-  __device__ void init(uint32_t size) {   // one thread, before the cluster's first barrier
-    bar_init(&bar, 1);
-    bar_expect(&bar, size * kWarps * 8);
-  }
-  // v of every lane (the same) to every CTA
-  __device__ __forceinline__ void post(uint64_t v, uint32_t rank, uint32_t size) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (lane < (int)size)
+  __device__ __forceinline__ void ready() const { bar_expect(bar, bytes); }   // one thread, for the next time
+  // v (the same in every lane) for segment `at` of the row to every CTA
+  __device__ __forceinline__ void post(int32_t at, uint64_t v, uint32_t size) const {
+    const uint32_t lane = threadIdx.x & 31;
+    if (lane < size)
       asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.u64 [%0], %1, [%2];" ::"r"(
-                       remote(&box[rank * kWarps + warp], lane)),
-                   "l"(v), "r"(remote(&bar, lane))
+                       remote(&box[at], lane)),
+                   "l"(v), "r"(remote(bar, lane))
                    : "memory");
-  }
-  // waits for all warps' values; the thread that says so readies the barrier for the next time
-  __device__ __forceinline__ bool wait(uint32_t parity, uint32_t size) {
-    const bool ok = bar_wait(&bar, parity);
-    if (threadIdx.x == 0) bar_expect(&bar, size * kWarps * 8);
-    return ok;
   }
 };
 
-// Where a row's slice of this CTA lies.
-template <typename T, int NT>
+// Where a CTA's slice of a row lies.
+template <typename T>
 struct Stream {
   static constexpr int kE = Elem<T>::kPerVec;
-  static constexpr int kWarps = NT / 32;
-  const T *p;          // the row
   int32_t vocab, off;
-  int32_t begin, n;    // this CTA's first vector, and how many it has
+  int32_t steps;       // of the row
+  int32_t begin, n;    // the first vector, and how many there are (whole steps, but for the row's end)
   uint4 *buf;
 
-  __device__ __forceinline__ void set(const T *row, int32_t v, int32_t blocks, uint32_t rank, uint4 *b) {
-    p = row;
+  // where a share of 2^log2 equal ones of the row's steps begins
+  __device__ __forceinline__ int32_t step_of(uint32_t share, int log2) const {
+    return (int32_t)(((uint64_t)steps * share) >> log2);
+  }
+  __device__ __forceinline__ void set(const T *row, int32_t v, uint32_t rank, int log2_size, uint4 *b) {
     vocab = v;
-    off = (int32_t)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
+    off = (int32_t)((uint32_t)reinterpret_cast<uintptr_t>(row) & 15u) / (int)sizeof(T);
     const int32_t vecs = (off + v + kE - 1) / kE;
-    begin = min(blocks * 128 * (int32_t)rank, vecs);
-    n = min(blocks * 128, vecs - begin);
+    steps = (vecs + 31) / 32;
+    begin = step_of(rank, log2_size) * 32;
+    n = min(step_of(rank + 1, log2_size) * 32, vecs) - begin;
     buf = b;
-  }
-  __device__ __forceinline__ bool cut_head() const { return off > 0 && begin == 0 && n > 0; }
-  __device__ __forceinline__ bool cut_tail() const { return n > 0 && (begin + n) * kE - off > vocab; }
-  // one thread: the copy of the vectors that lie inside the row
-  __device__ __forceinline__ void copy(uint64_t *full) const {
-    const int32_t from = cut_head() ? 1 : 0, to = n - (cut_tail() ? 1 : 0);
-    const uint32_t bytes = to > from ? (uint32_t)(to - from) * 16 : 0;
-    bar_expect(full, bytes);
-    if (bytes)
-      asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                       smem(buf + from)),
-                   "l"(p + (begin + from) * kE - off), "r"(bytes), "r"(smem(full))
-                   : "memory");
-  }
-  __device__ __forceinline__ bool owns(int32_t vec) const {
-    return (vec >> 7) % kWarps == (int32_t)(threadIdx.x >> 5) && (vec & 31) == (int32_t)(threadIdx.x & 31);
-  }
-  __device__ __forceinline__ uint4 by_elements(int32_t vec) const {
-    float x[kE];
-    const int32_t i = (begin + vec) * kE - off;
-#pragma unroll
-    for (int e = 0; e < kE; e++) x[e] = i + e >= 0 && i + e < vocab ? Elem<T>::load(p + i + e) : -INFINITY;
-    return Elem<T>::pack(x);
-  }
-  // the vectors that stick out, read by their owner into `head` and `tail` ...
-  __device__ __forceinline__ void read_edges(uint4 &head, uint4 &tail) const {
-    if (cut_head() && owns(0)) head = by_elements(0);
-    if (cut_tail() && owns(n - 1)) tail = by_elements(n - 1);
-  }
-  // ... and put into the buffer, where only the owner reads them
-  __device__ __forceinline__ void put_edges(uint4 head, uint4 tail) const {
-    const bool h = cut_head() && owns(0), t = cut_tail() && owns(n - 1);
-    if (h) buf[0] = head;
-    if (t) buf[n - 1] = tail;
-    if (h || t) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // a later copy may write these places
   }
   __device__ __forceinline__ int32_t index(int32_t vec, int e) const { return (begin + vec) * kE + e - off; }
 
-  // f(first vector's place, four vectors): this thread's share of each block;
-  // what is not in the row is -inf
-  template <typename F>
-  __device__ __forceinline__ void blocks(F f) const {
-    constexpr uint32_t ninf = Elem<T>::kNegInf;
+  // the producer warp: brings `row` in; `full` counts two arrivals
+  __device__ __forceinline__ void bring(const T *row, uint64_t *full) const {
     const int lane = threadIdx.x & 31;
-    for (int32_t b = (int32_t)(threadIdx.x >> 5) * 128; b < n; b += kWarps * 128) {
-      uint4 v[4];
-      if (b + 128 <= n) {
-#pragma unroll
-        for (int s = 0; s < 4; s++) v[s] = buf[b + s * 32 + lane];
-      } else {
-#pragma unroll
-        for (int s = 0; s < 4; s++)
-          v[s] = b + s * 32 + lane < n ? buf[b + s * 32 + lane] : make_uint4(ninf, ninf, ninf, ninf);
+    const bool head = off > 0 && begin == 0 && n > 0, tail = n > 0 && index(n, 0) > vocab;
+    const int32_t from = head ? 1 : 0, to = n - (tail ? 1 : 0);
+    if (lane == 0) {
+      // (what was written to the buffer element by element, some rows ago, comes before the copy)
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      const uint32_t bytes = to > from ? (uint32_t)(to - from) * 16 : 0;
+      bar_expect(full, bytes);
+      if (bytes)
+        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                         smem(buf + from)),
+                     "l"(row + index(from, 0)), "r"(bytes), "r"(smem(full))
+                     : "memory");
+    }
+    constexpr uint32_t ninf = Elem<T>::kNegInf;
+    if (lane >= (n & 31) && (n & 31)) buf[(n & ~31) + lane] = make_uint4(ninf, ninf, ninf, ninf);
+    if (head || tail) {
+      const int e = lane & 15;
+      const int32_t vec = lane < 16 ? 0 : n - 1;
+      if (e < kE && (lane < 16 ? head : tail)) {
+        const int32_t i = index(vec, e);
+        Elem<T>::store(reinterpret_cast<T *>(buf + vec) + e, i >= 0 && i < vocab ? Elem<T>::load(row + i) : -INFINITY);
       }
-      f(b + lane, v);
     }
+    __syncwarp();
+    if (lane == 0) bar_arrive(full);
   }
-  // writes vector `vec` to the same place of another row
-  __device__ __forceinline__ void write(T *row, bool aligned, int32_t vec, const float *x) const {
-    if (vec >= n) return;
-    const int32_t i = (begin + vec) * kE - off;
-    if (aligned && i >= 0 && i + kE <= vocab) {
-      *reinterpret_cast<uint4 *>(row + i) = Elem<T>::pack(x);
-    } else {
+  // whether step `st` of the slice lies inside the row, all of it
+  __device__ __forceinline__ bool inside(int32_t st) const {
+    return index(st * 32, 0) >= 0 && index(st * 32 + 32, 0) <= vocab;
+  }
+  // writes the elements of vector `vec` that are in the row
+  __device__ __forceinline__ void write_edge(T *row, int32_t vec, const float *x) const {
+    const int32_t i = index(vec, 0);
 #pragma unroll
-      for (int e = 0; e < kE; e++)
-        if (i + e >= 0 && i + e < vocab) Elem<T>::store(row + i + e, x[e]);
-    }
+    for (int e = 0; e < kE; e++)
+      if (vec < n && i + e >= 0 && i + e < vocab) Elem<T>::store(row + i + e, x[e]);
   }
 };
 
