@@ -54,44 +54,60 @@ def _entries():
     return L
 
 
-def _call(device, stream, entry, *args):
-    """Calls an entry on `device`, its last argument the stream's handle."""
-    fn = getattr(_entries(), entry)
+# the current stream's handle without a Stream object around it, where torch has that
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _call(index, stream, fn, *args):
+    """Calls an entry on device `index`, its last argument the stream's handle."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, handle))
+        handle = _current_stream(index)
     else:
-        with torch.cuda.device(device):
-            _check(fn(*args, handle))
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if index == torch.cuda.current_device():
+        rc = fn(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, handle)
+    if rc:
+        _check(rc)
 
 
-def _new(shape, dtype, device, stream):
-    """An output's memory; where another stream than the current one writes it, the allocator is told."""
-    t = torch.empty(shape, dtype=dtype, device=device)
+def _new(shape, dtype, like, stream):
+    """An output's memory beside `like`; where another stream than the current one writes it, the allocator is told."""
+    t = torch.empty(shape, dtype=dtype, device=like.device)
     if stream is not None:
         t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
-                        torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream), device=device))
+                        torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream), device=like.device))
     return t
 
 
 def _logits(x, name="logits"):
-    """rows, vocab, row stride, dtype code of a 2-D tensor whose rows are contiguous."""
-    if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dtype in _DTYPES and x.dim() == 2):
+    """rows, vocab, row stride, dtype code and device index of a 2-D tensor whose rows are contiguous."""
+    dtype = _DTYPES.get(x.dtype) if isinstance(x, torch.Tensor) and x.is_cuda else None
+    if dtype is None or x.dim() != 2:
         raise TypeError(f"{name} must be a 2-D CUDA tensor of float32, float16 or bfloat16")
     rows, vocab = x.shape
     stride, unit = x.stride()
     if unit != 1 and vocab > 1:
         raise TypeError(f"{name} must have contiguous rows (stride 1 in the last dimension)")
-    return rows, vocab, stride if rows > 1 else vocab, _DTYPES[x.dtype]
+    return rows, vocab, stride if rows > 1 else vocab, dtype, x.get_device()
 
 
-def _vector(t, name, rows, dtype, device):
-    if not (isinstance(t, torch.Tensor) and t.device == device and t.dtype == dtype and t.is_contiguous()
-            and t.shape == (rows,)):
-        raise TypeError(f"{name} must be a contiguous {dtype} tensor of {rows} entries on {device}")
+def _vector(t, name, n, dtype, index):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.dim() == 1
+            and t.shape[0] == n and t.is_contiguous()):
+        raise TypeError(f"{name} must be a contiguous {dtype} tensor of {n} entries on cuda:{index}")
     return t.data_ptr()
+
+
+def _output(t, name, n, dtype, index, like, stream):
+    """A given output, checked, or a new one: the tensor and its address."""
+    if t is None:
+        t = _new(n, dtype, like, stream)
+        return t, t.data_ptr()
+    return t, _vector(t, name, n, dtype, index)
 
 
 def sample_tokens(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tokens=None, logps=None, stream=None):
@@ -103,21 +119,22 @@ def sample_tokens(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tok
     greedy; top_k <= 0, top_p >= 1 and min_p <= 0 are off.  The filters apply
     in the order top-k, top-p, min-p.  The sums are integers: a row's token
     does not depend on the batch it is in."""
-    rows, vocab, stride, dtype = _logits(logits)
-    device = logits.device
-    s = _Sampling()
+    rows, vocab, stride, dtype, index = _logits(logits)
+    one, each = [], []
     for (name, kind), v in zip(_SETTINGS, (temperature, top_k, top_p, min_p)):
         if isinstance(v, torch.Tensor):
-            setattr(s, name + "s", _vector(v, name, rows, kind, device))
+            each.append(_vector(v, name, rows, kind, index))
+            one.append(0)
         elif v != v:
             raise ValueError(f"{name} is NaN")
         else:
-            setattr(s, name, min(max(int(v), 0), 2 ** 31 - 1) if name == "top_k" else float(v))
-    up = _vector(u, "u", rows, torch.float32, device)
-    tokens = _new(rows, torch.int64, device, stream) if tokens is None else tokens
-    logps = _new(rows, torch.float32, device, stream) if logps is None else logps
-    _call(device, stream, "seqsum_sample_tokens", logits.data_ptr(), dtype, rows, vocab, stride, up, s,
-          _vector(tokens, "tokens", rows, torch.int64, device), _vector(logps, "logps", rows, torch.float32, device))
+            each.append(None)
+            one.append(min(max(int(v), 0), 2 ** 31 - 1) if name == "top_k" else v)
+    up = _vector(u, "u", rows, torch.float32, index)
+    tokens, tp = _output(tokens, "tokens", rows, torch.int64, index, logits, stream)
+    logps, lp = _output(logps, "logps", rows, torch.float32, index, logits, stream)
+    _call(index, stream, _entries().seqsum_sample_tokens, logits.data_ptr(), dtype, rows, vocab, stride, up,
+          _Sampling(*one, *each), tp, lp)
     return tokens, logps
 
 
@@ -125,21 +142,20 @@ def token_logprob(logits, tokens, logps=None, lses=None, stream=None):
     """(logps, lses), float32: the log-probability of each row's token and the
     row's log of the sum of exponentials.  A token outside [0, vocab) marks an
     unused row: its logp is 0."""
-    rows, vocab, stride, dtype = _logits(logits)
-    device = logits.device
-    tp = _vector(tokens, "tokens", rows, torch.int64, device)
-    logps = _new(rows, torch.float32, device, stream) if logps is None else logps
-    lses = _new(rows, torch.float32, device, stream) if lses is None else lses
-    _call(device, stream, "seqsum_token_logprob", logits.data_ptr(), dtype, rows, vocab, stride, tp,
-          _vector(logps, "logps", rows, torch.float32, device), _vector(lses, "lses", rows, torch.float32, device))
+    rows, vocab, stride, dtype, index = _logits(logits)
+    tp = _vector(tokens, "tokens", rows, torch.int64, index)
+    logps, lp = _output(logps, "logps", rows, torch.float32, index, logits, stream)
+    lses, sp = _output(lses, "lses", rows, torch.float32, index, logits, stream)
+    _call(index, stream, _entries().seqsum_token_logprob, logits.data_ptr(), dtype, rows, vocab, stride, tp, lp, sp)
     return logps, lses
 
 
 def _gradient(out, logits, stream):
     """The gradient's tensor and its row stride: apart from the logits, or the logits themselves."""
     if out is None:
-        out = _new(logits.shape, logits.dtype, logits.device, stream)
-    rows, vocab, stride, _ = _logits(out, "out")
+        rows, vocab = logits.shape
+        return _new((rows, vocab), logits.dtype, logits, stream), vocab
+    rows, vocab, stride, _, _ = _logits(out, "out")
     if out.shape != logits.shape or out.dtype != logits.dtype or out.device != logits.device:
         raise TypeError("out must have the logits' shape, type and device")
     if rows > 1 and stride < vocab:
@@ -151,30 +167,27 @@ def token_logprob_grad(logits, tokens, dlogps, out=None, logps=None, lses=None, 
     """(dlogits, logps, lses): token_logprob and, from the same read of the
     logits, the gradient of (dlogps * logps).sum() with respect to them.
     `out` may be the logits."""
-    rows, vocab, stride, dtype = _logits(logits)
-    device = logits.device
-    tp = _vector(tokens, "tokens", rows, torch.int64, device)
-    gp = _vector(dlogps, "dlogps", rows, torch.float32, device)
+    rows, vocab, stride, dtype, index = _logits(logits)
+    tp = _vector(tokens, "tokens", rows, torch.int64, index)
+    gp = _vector(dlogps, "dlogps", rows, torch.float32, index)
     out, ostride = _gradient(out, logits, stream)
-    logps = _new(rows, torch.float32, device, stream) if logps is None else logps
-    lses = _new(rows, torch.float32, device, stream) if lses is None else lses
-    _call(device, stream, "seqsum_token_logprob_grad", logits.data_ptr(), dtype, rows, vocab, stride, tp, gp,
-          out.data_ptr(), ostride, _vector(logps, "logps", rows, torch.float32, device),
-          _vector(lses, "lses", rows, torch.float32, device))
+    logps, lp = _output(logps, "logps", rows, torch.float32, index, logits, stream)
+    lses, sp = _output(lses, "lses", rows, torch.float32, index, logits, stream)
+    _call(index, stream, _entries().seqsum_token_logprob_grad, logits.data_ptr(), dtype, rows, vocab, stride, tp, gp,
+          out.data_ptr(), ostride, lp, sp)
     return out, logps, lses
 
 
 def token_logprob_backward(logits, tokens, dlogps, lses, out=None, stream=None):
     """dlogits: the gradient of (dlogps * logps).sum() with respect to the
     logits, from the lses that token_logprob returned.  `out` may be the logits."""
-    rows, vocab, stride, dtype = _logits(logits)
-    device = logits.device
-    tp = _vector(tokens, "tokens", rows, torch.int64, device)
-    gp = _vector(dlogps, "dlogps", rows, torch.float32, device)
-    lp = _vector(lses, "lses", rows, torch.float32, device)
+    rows, vocab, stride, dtype, index = _logits(logits)
+    tp = _vector(tokens, "tokens", rows, torch.int64, index)
+    gp = _vector(dlogps, "dlogps", rows, torch.float32, index)
+    lp = _vector(lses, "lses", rows, torch.float32, index)
     out, ostride = _gradient(out, logits, stream)
-    _call(device, stream, "seqsum_token_logprob_backward", logits.data_ptr(), dtype, rows, vocab, stride, tp, gp, lp,
-          out.data_ptr(), ostride)
+    _call(index, stream, _entries().seqsum_token_logprob_backward, logits.data_ptr(), dtype, rows, vocab, stride, tp, gp,
+          lp, out.data_ptr(), ostride)
     return out
 
 
@@ -232,21 +245,23 @@ class TensorList:
     def _out(self, out, stream):
         if self._h is None:
             raise SeqsumError("seqsum: the list was closed")
-        if out is None:
-            out = _new(1, torch.float32, self._device, stream)
-        return out, _vector(out, "out", 1, torch.float32, self._device)
+        return _output(out, "out", 1, torch.float32, self._device.index, self, stream)
+
+    @property
+    def device(self):
+        return self._device
 
     def norm(self, scale: float = 1.0, out=None, stream=None):
         """scale * the 2-norm of all numbers of the list (a 1-element float32 tensor)."""
         out, p = self._out(out, stream)
-        _call(self._device, stream, "seqsum_tensors_norm", self._h, float(scale), p)
+        _call(self._device.index, stream, _entries().seqsum_tensors_norm, self._h, scale, p)
         return out
 
     def clip(self, max_norm: float, scale: float = 1.0, out=None, stream=None):
         """Writes every number times scale * min(1, max_norm / (norm + 1e-6))
         and returns the norm (of the scaled numbers, before clipping)."""
         out, p = self._out(out, stream)
-        _call(self._device, stream, "seqsum_tensors_clip", self._h, float(max_norm), float(scale), p)
+        _call(self._device.index, stream, _entries().seqsum_tensors_clip, self._h, max_norm, scale, p)
         return out
 
     def close(self):
