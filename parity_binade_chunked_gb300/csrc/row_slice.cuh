@@ -146,6 +146,11 @@ __device__ __forceinline__ uint64_t ld_remote64(uint32_t a) {
   asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
   return v;
 }
+__device__ __forceinline__ uint4 ld_remote128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
 __device__ __forceinline__ uint32_t ld_remote32(uint32_t a) {
   uint32_t v;
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
@@ -176,12 +181,13 @@ __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
   return v;
 }
-__device__ __forceinline__ float warp_max_all(float v) {
-  // floats as unsigned integers of the same order
-  const uint32_t b = __float_as_uint(v), k = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
-  const uint32_t m = __reduce_max_sync(~0u, k);
-  return __uint_as_float(m & 0x80000000u ? m ^ 0x80000000u : ~m);
+// floats as unsigned integers of the same order, and back
+__device__ __forceinline__ uint32_t ordered(float v) {
+  const uint32_t b = __float_as_uint(v);
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
+__device__ __forceinline__ float from_ordered(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
+__device__ __forceinline__ float warp_max_all(float v) { return from_ordered(__reduce_max_sync(~0u, ordered(v))); }
 __device__ __forceinline__ float warp_add(float v) {   // the same tree in every lane
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
@@ -357,6 +363,16 @@ static __device__ __noinline__ bool bar_wait_long(uint64_t *bar, uint32_t parity
 // false: gave up
 __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity) {
   return bar_try(bar, parity) || bar_wait_long(bar, parity);
+}
+
+// One arrival of the calling warp at `bar` of every CTA: what its lanes wrote
+// to shared memory before is seen by who waits for it.  A barrier of the
+// cluster's working warps needs two such in turn.
+__device__ __forceinline__ void arrive_everywhere(uint64_t *bar, uint32_t size) {
+  const uint32_t lane = threadIdx.x & 31;
+  __syncwarp();
+  if (lane < size)
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote(bar, lane)) : "memory");
 }
 
 struct Exchange {

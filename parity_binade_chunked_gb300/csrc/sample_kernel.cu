@@ -13,6 +13,8 @@
 // Entries with d <= -32 have w = 0 and can be left out everywhere.
 #include <math.h>
 
+#include <atomic>
+
 #include "../../include/seqsum.h"
 #include "row_slice.cuh"
 
@@ -32,6 +34,7 @@ struct SampleArgs {
   seqsum_sampling s;
   int64_t *tokens;
   float *logps;
+  int32_t steps;   // that a CTA takes of a row at most
 };
 
 // A place in the order: an entry is before it where its key (the bits of -d)
@@ -59,6 +62,22 @@ __device__ __forceinline__ uint64_t share(uint64_t part, uint64_t whole) {
   return (__umul64hi(part, whole) << 32) | ((part * whole) >> 32);
 }
 
+// floor(2^32 * x) for x in [0, 1]
+__device__ __forceinline__ uint64_t part_of(float x) { return x > 0.0f ? (uint64_t)(x * 4294967296.0f) : 0; }
+
+// 2^31 * 2^d as an integer: 0 for d <= kFloor, and for NaN
+__device__ __forceinline__ uint32_t weight(float d) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(d));
+  return __float2uint_rn(y * 2147483648.0f);
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t key_of(float d) { return __float_as_uint(d) & 0x7fffffffu; }
+
 // Sum over the CTA's threads, in every thread.  sh.warp is free again after the next barrier.
 template <int NT>
 __device__ __forceinline__ uint64_t block_sum(uint64_t v, Shared &sh) {
@@ -71,9 +90,12 @@ __device__ __forceinline__ uint64_t block_sum(uint64_t v, Shared &sh) {
   return t;
 }
 
-template <typename T, int KV, int NT>
+// ---- rows too large for the buffers: one CTA a part of a row, every pass reads
+// global memory (L2), and every search goes over the whole row.
+
+template <typename T, int NT>
 struct Sampler {
-  Slice<T, KV, NT> x;
+  Slice<T, 0, NT> x;
   Shared &sh;
   float m, c;
   uint32_t rank, size;
@@ -82,8 +104,6 @@ struct Sampler {
 
   // octaves below the maximum; NaN (a masked logit where c is 0, a NaN logit) counts as masked
   __device__ __forceinline__ float octaves(float v) const { return v == m ? 0.0f : (v - m) * c; }
-  __device__ __forceinline__ static uint32_t weight(float d) { return __float2uint_rn(exp2f(d) * 2147483648.0f); }
-  __device__ __forceinline__ static uint32_t key(float d) { return __float_as_uint(d) & 0x7fffffffu; }
 
   // f(d, index) for every entry whose weight may be above 0
   template <typename F>
@@ -182,12 +202,12 @@ struct Sampler {
       clear(1);
       if (!ties) {
         entries([&](float d, int32_t) {
-          const uint32_t q = key(d);
+          const uint32_t q = key_of(d);
           if (q >= lo && q < hi) put(1, (q - lo) >> shift, d);
         });
       } else {
         entries([&](float d, int32_t i) {
-          if (key(d) == lo && i >= ilo && i < ihi) put(1, (i - ilo) >> shift, d);
+          if (key_of(d) == lo && i >= ilo && i < ihi) put(1, (i - ilo) >> shift, d);
         });
       }
       search(1, by_mass, need);
@@ -202,16 +222,15 @@ struct Sampler {
   }
 };
 
-template <typename T, int KV, int NT>
-__global__ __launch_bounds__(NT) void sample_kernel(const SampleArgs a) {
+template <typename T, int NT>
+__global__ __launch_bounds__(NT) void sample_reread_kernel(const SampleArgs a) {
   __shared__ Shared sh;
   const uint32_t size = cluster_size(), rank = cluster_rank();
   const int64_t row = blockIdx.x / size;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  Sampler<T, KV, NT> s(sh);
+  Sampler<T, NT> s(sh);
   s.rank = rank, s.size = size;
   s.x.set(static_cast<const T *>(a.logits) + row * a.stride, a.vocab, rank, size);
-  s.x.load();
 
   const float temperature = a.s.temperatures ? a.s.temperatures[row] : a.s.temperature;
   const int32_t top_k = a.s.top_ks ? a.s.top_ks[row] : a.s.top_k;
@@ -278,7 +297,7 @@ __global__ __launch_bounds__(NT) void sample_kernel(const SampleArgs a) {
 
   // the kept mass: of this thread, its warp, its CTA, the row
   auto kept = [&](float d, int32_t i) -> uint32_t {
-    const uint32_t w = s.weight(d), q = s.key(d);
+    const uint32_t w = weight(d), q = key_of(d);
     return w >= least && (q < end.key || (q == end.key && i < end.index)) ? w : 0;
   };
   uint64_t mine = 0;
@@ -333,27 +352,668 @@ __global__ __launch_bounds__(NT) void sample_kernel(const SampleArgs a) {
   });
 }
 
-template <typename T, int KV, int NT>
-int run_sample(const SampleArgs &a, int size, cudaStream_t stream) {
-  const cudaError_t e = launch_rows(sample_kernel<T, KV, NT>, a, a.rows, size, NT, 0, stream);
+// ---- rows streamed through shared memory (see Stream)
+
+constexpr int kList = 2048;   // entries that a search can take out of the row
+
+template <int W>
+struct Picks {
+  static constexpr int kBoxes = kMaxCluster * W;
+  uint64_t full[2], empty[2], told[2], gate[2];
+  uint64_t box[2][kBoxes];        // a word of every warp of the cluster
+  uint64_t mass[W], above[W];     // of the warps' entries; of those before the listed ones
+  uint32_t heads[kBins];          // entries by eighths of an octave
+  uint4 bins[2][kBins];           // a split: count, and mass in two halves
+  uint32_t bin_count[kBins];      // ... summed over whom it concerns
+  uint64_t bin_mass[kBins];
+  uint32_t listed, small_listed;
+  uint2 small[32];                // the last few entries of a search
+  uint2 list[kList], all[kList];  // (key, index): this CTA's entries, the row's
+};
+
+struct Found {
+  int bin;                        // -1: the need is not reached
+  uint32_t count, count_before;
+  uint64_t mass, mass_before;
+};
+
+template <typename T, int W>
+struct Picker {
+  static constexpr int kE = Elem<T>::kPerVec, kThreads = W * 32;
+  Picks<W> &sh;
+  Stream<T> x;
+  uint32_t rank, size, told = 0, gated = 0;
+  int32_t st0, st1;     // this warp's steps
+  float m, c;
+  bool special;         // (v - m) * c needs care
+  bool ok = true;
+  int32_t listed = -1;  // entries of sh.all, once a search goes over those; -1: over the row
+
+  __device__ Picker(Picks<W> &s) : sh(s) {}
+
+  // ---- the CTA's working warps, and the cluster's
+
+  __device__ __forceinline__ void team() const { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kThreads) : "memory"); }
+  // all of the CTA's working warps go on together or give up together
+  __device__ __forceinline__ void agree(bool mine) {
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"((uint32_t)mine), "n"(kThreads)
+        : "memory");
+    ok &= all != 0;
+  }
+  // every warp's word to every warp: in the box that is returned
+  __device__ __forceinline__ const uint64_t *tell(uint64_t v) {
+    const uint32_t b = told & 1, parity = (told >> 1) & 1;
+    told++;
+    const Exchange e = {sh.box[b], &sh.told[b], size * W * 8};
+    e.post((int32_t)(rank * W + (threadIdx.x >> 5)), v, size);
+    const bool came = bar_wait(e.bar, parity);
+    if (threadIdx.x == 0) e.ready();
+    agree(came);
+    return sh.box[b];
+  }
+  // what any working thread of the cluster wrote to shared memory before is seen after
+  __device__ __forceinline__ void gather() {
+    uint64_t *bar = &sh.gate[gated & 1];
+    const uint32_t parity = (gated >> 1) & 1;
+    gated++;
+    arrive_everywhere(bar, size);
+    agree(bar_wait(bar, parity));
+  }
+
+  // ---- entries
+
+  __device__ __forceinline__ void octaves(uint4 w, float *d) const {
+    Elem<T>::unpack(w, d);
+    if (special) {
+#pragma unroll
+      for (int e = 0; e < kE; e++) d[e] = d[e] == m ? 0.0f : (d[e] - m) * c;
+    } else {
+      const uint64_t mm = pair(-m, -m), cc = pair(c, c);
+#pragma unroll
+      for (int e = 0; e < kE; e += 2) split(mul2(add2(pair(d[e], d[e + 1]), mm), cc), d[e], d[e + 1]);
+    }
+  }
+  // f(octaves, index) of the row's entries above `from` (at least kFloor) in this thread
+  template <typename F>
+  __device__ __forceinline__ void row_entries(float from, F f) const {
+    const int lane = threadIdx.x & 31;
+    for (int32_t st = st0; st < st1; st++) {
+      float d[kE];
+      octaves(x.buf[st * 32 + lane], d);
+#pragma unroll
+      for (int e = 0; e < kE; e++)
+        if (d[e] >= from && d[e] > kFloor) f(d[e], x.index(st * 32 + lane, e));
+    }
+  }
+  // ... or, once there is one, of the list
+  template <typename F>
+  __device__ __forceinline__ void entries(F f) const {
+    if (listed < 0) {
+      row_entries(kFloor, f);
+    } else {
+      for (int32_t i = threadIdx.x; i < listed; i += kThreads) {
+        const uint2 v = sh.all[i];
+        f(-__uint_as_float(v.x), (int32_t)v.y);
+      }
+    }
+  }
+
+  // ---- searches
+
+  __device__ __forceinline__ void put(uint4 *bins, uint32_t bin, float d) const {
+    const uint32_t w = weight(d);
+    atomicAdd(&bins[bin].x, 1u);
+    atomicAdd(&bins[bin].y, w & 0xffffu);   // a CTA has less than 2^16 entries: the halves' sums fit 32 bits
+    atomicAdd(&bins[bin].z, w >> 16);
+  }
+  // Entries by bin_of(key, index), where that is below kBins, and the first
+  // bin at which their count (or mass) reaches `need`.
+  template <typename B>
+  __device__ Found find(bool by_mass, uint64_t need, B bin_of) {
+    uint4 *bins = sh.bins[gated & 1];   // (in turn: others of the cluster may still read the last one)
+    if (threadIdx.x < kBins) bins[threadIdx.x] = make_uint4(0, 0, 0, 0);
+    team();
+    entries([&](float d, int32_t i) {
+      const uint32_t b = bin_of(key_of(d), i);
+      if (b < (uint32_t)kBins) put(bins, b, d);
+    });
+    if (listed < 0) gather();
+    else team();
+    if (threadIdx.x < kBins) {
+      uint32_t n = 0;
+      uint64_t w = 0;
+      if (listed < 0) {
+        for (uint32_t r = 0; r < size; r++) {
+          const uint4 v = ld_remote128(remote(&bins[threadIdx.x], r));
+          n += v.x, w += v.y + ((uint64_t)v.z << 16);
+        }
+      } else {
+        const uint4 v = bins[threadIdx.x];
+        n = v.x, w = v.y + ((uint64_t)v.z << 16);
+      }
+      sh.bin_count[threadIdx.x] = n;
+      sh.bin_mass[threadIdx.x] = w;
+    }
+    team();
+    // every warp for itself: lane l has bins 8 l to 8 l + 7
+    constexpr int kPer = kBins / 32;
+    const int lane = threadIdx.x & 31;
+    uint64_t n = 0, w = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; i++) n += sh.bin_count[lane * kPer + i], w += sh.bin_mass[lane * kPer + i];
+    const uint64_t v = by_mass ? w : n, upto = warp_scan(v, lane);
+    const uint32_t owner = __ballot_sync(~0u, upto - v < need && need <= upto);
+    Found f;
+    f.bin = -1;
+    uint64_t nb = warp_scan(n, lane) - n, wb = warp_scan(w, lane) - w;
+    if (owner == 0) {
+      f.count = f.count_before = 0;
+      f.mass = 0, f.mass_before = __shfl_sync(~0u, wb + w, 31);
+    } else {
+      int b = lane * kPer;
+      uint32_t bn = 0;
+      uint64_t bw = 0;
+      if (owner >> lane & 1) {
+        for (;; b++) {
+          bn = sh.bin_count[b], bw = sh.bin_mass[b];
+          if ((by_mass ? wb + bw : nb + bn) >= need) break;
+          nb += bn, wb += bw;
+        }
+      }
+      const int o = __ffs(owner) - 1;
+      f.bin = __shfl_sync(~0u, b, o);
+      f.count = __shfl_sync(~0u, bn, o), f.count_before = __shfl_sync(~0u, (uint32_t)nb, o);
+      f.mass = __shfl_sync(~0u, bw, o), f.mass_before = __shfl_sync(~0u, wb, o);
+    }
+    team();   // the sums may be written again
+    return f;
+  }
+
+  // The end of the shortest prefix of the entries' order that has `need`
+  // entries (or `need` of mass), and its mass; without one the end of all.
+  // The entries' eighths of octaves lie in [eighth0, eighth1).
+  __device__ Place prefix(bool by_mass, uint64_t need, int eighth0, int eighth1, uint64_t *mass) {
+    // The first split is even in octaves: by a power of two, from an eighth, so
+    // that differences and products are exact and each bin is a range of keys.
+    float scale = 8.0f;
+    for (int n = eighth1 - eighth0; n <= kBins / 2; n *= 2) scale *= 2.0f;
+    const float from = eighth0 * 0.125f;
+    uint32_t lo = __float_as_uint(from), hi = __float_as_uint(eighth1 * 0.125f);
+    Found f = find(by_mass, need, [&](uint32_t key, int32_t) {
+      return key >= lo && key < hi ? (uint32_t)((__uint_as_float(key) - from) * scale) : (uint32_t)kBins;
+    });
+    if (f.bin < 0) {
+      *mass = f.mass_before;
+      return Place{0x7fffffffu, 0};
+    }
+    lo = __float_as_uint(from + f.bin / scale), hi = __float_as_uint(from + (f.bin + 1) / scale);
+    int32_t ilo = 0, ihi = x.vocab;
+    uint64_t before = 0;
+    while (ok) {
+      need -= by_mass ? f.mass_before : (uint64_t)f.count_before;
+      before += f.mass_before;
+      const bool ties = hi - lo == 1;
+      if (f.count == 1 || (by_mass ? need == f.mass : need == f.count)) {
+        *mass = before + f.mass;
+        return ties ? Place{lo, ihi} : Place{hi, 0};
+      }
+      auto inside = [&](uint32_t key, int32_t i) { return ties ? key == lo && i >= ilo && i < ihi : key >= lo && key < hi; };
+      if (listed >= 0 && f.count <= 32) return last_few(by_mass, need, before, f.count, inside, mass);
+      // split keys [lo, hi), or, where that is one key, its indices [ilo, ihi)
+      const uint32_t width = ties ? (uint32_t)(ihi - ilo) : hi - lo;
+      const int shift = max(0, 32 - __clz(width - 1) - 8);
+      f = find(by_mass, need, [&](uint32_t key, int32_t i) {
+        return inside(key, i) ? (ties ? (uint32_t)(i - ilo) : key - lo) >> shift : (uint32_t)kBins;
+      });
+      if (f.bin < 0) break;   // (cannot be: the bin reached the need)
+      if (ties) {
+        ilo += f.bin << shift;
+        ihi = min(ihi, ilo + (1 << shift));
+      } else {
+        lo += (uint32_t)f.bin << shift;
+        hi = min(hi, lo + (1u << shift));
+      }
+    }
+    *mass = before;
+    return Place{hi, 0};
+  }
+
+  // At most 32 listed entries, `n` of them: each lane one, placed by counting.
+  template <typename I>
+  __device__ Place last_few(bool by_mass, uint64_t need, uint64_t before, uint32_t n, I inside, uint64_t *mass) {
+    if (threadIdx.x == 0) sh.small_listed = 0;
+    team();
+    entries([&](float d, int32_t i) {
+      const uint32_t key = key_of(d);
+      if (inside(key, i)) {
+        const uint32_t at = atomicAdd(&sh.small_listed, 1u);
+        if (at < 32) sh.small[at] = make_uint2(key, (uint32_t)i);
+      }
+    });
+    team();
+    const uint32_t lane = threadIdx.x & 31;
+    const bool have = lane < n;
+    const uint2 v = have ? sh.small[lane] : make_uint2(~0u, ~0u);
+    const uint32_t w = have ? weight(-__uint_as_float(v.x)) : 0;
+    uint32_t count = 0;
+    uint64_t sum = 0;
+    for (uint32_t j = 0; j < n; j++) {
+      const uint32_t kj = __shfl_sync(~0u, v.x, j), ij = __shfl_sync(~0u, v.y, j), wj = __shfl_sync(~0u, w, j);
+      if (kj < v.x || (kj == v.x && ij < v.y)) count++, sum += wj;
+    }
+    const bool last = have && (by_mass ? sum < need && need <= sum + w : count + 1 == need);
+    const int o = max(0, __ffs(__ballot_sync(~0u, last)) - 1);
+    *mass = before + __shfl_sync(~0u, sum + w, o);
+    const Place p = {__shfl_sync(~0u, v.x, o), (int32_t)__shfl_sync(~0u, v.y, o) + 1};
+    team();
+    return p;
+  }
+
+  // ---- the kept prefix
+
+  // Where the prefix that top-k and top-p keep ends.  `least` is a lower bound
+  // of the k-th largest entry's octaves.
+  __device__ Place kept_prefix(int32_t top_k, bool by_p, float top_p, float least) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    bool by_k = top_k > 0 && top_k < x.vocab;
+    listed = -1;
+    // counts by eighths of octaves, and the mass of all that may be kept
+    if (threadIdx.x < kBins) sh.heads[threadIdx.x] = 0;
+    if (threadIdx.x == 0) sh.listed = 0;
+    team();
+    uint64_t mine = 0;
+    row_entries(least, [&](float d, int32_t) {
+      atomicAdd(&sh.heads[(int)(-d * 8.0f)], 1u);
+      if (by_p) mine += weight(d);
+    });
+    mine = warp_sum(mine);
+    if (lane == 0) sh.mass[warp] = mine;
+    gather();
+    if (threadIdx.x < kBins) {
+      uint32_t n = 0;
+      for (uint32_t r = 0; r < size; r++) n += ld_remote32(remote(&sh.heads[threadIdx.x], r));
+      sh.bin_count[threadIdx.x] = n;
+    }
+    uint64_t all = 0;
+    for (uint32_t i = lane; i < size * W; i += 32) all += ld_remote64(remote(&sh.mass[i % W], i / W));
+    all = warp_sum(all);
+    team();
+    constexpr int kPer = kBins / 32;
+    uint32_t counts[kPer], n = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; i++) n += counts[i] = sh.bin_count[lane * kPer + i];
+    const uint32_t upto = (uint32_t)warp_scan(n, lane), total = __shfl_sync(~0u, upto, 31);
+    if (by_k && total < (uint32_t)top_k) by_k = false;   // all that weighs anything is among the first k
+    if (!by_k && !by_p) return Place{0x7fffffffu, 0};
+
+    // the eighths that the search has to look at
+    int eighth0 = 0, eighth1 = kBins;
+    uint64_t cut = 0;
+    if (by_k) {
+      uint32_t before = upto - n;
+      int b = kBins;
+#pragma unroll
+      for (int i = kPer - 1; i >= 0; i--) {
+        // from the last bin of the lane to the first: the first whose count reaches k
+        uint32_t to = before;
+#pragma unroll
+        for (int j = 0; j <= i; j++) to += counts[j];
+        if (to >= (uint32_t)top_k) b = lane * kPer + i + 1;
+      }
+      eighth1 = __reduce_min_sync(~0u, (uint32_t)b);
+    } else {
+      if (all == 0) all = 1;
+      cut = max((uint64_t)1, share(part_of(top_p), all));
+      // Bounds of the mass before each eighth, from the counts: from its front
+      // and, what is narrower in the tail, from its back.
+      uint64_t least_mass = 0, most_mass = 0;
+      uint64_t lo[kPer], hi[kPer];
+#pragma unroll
+      for (int i = 0; i < kPer; i++) {
+        const int b = lane * kPer + i;
+        const float top = ex2(31.0f - b * 0.125f);
+        const uint64_t w1 = (uint64_t)(top * 1.00001f) + 2, w0 = (uint64_t)fmaxf(top * (0.9170040f * 0.99999f) - 2.0f, 0.0f);
+        lo[i] = counts[i] * w0, hi[i] = counts[i] * w1;
+        least_mass += lo[i], most_mass += hi[i];
+      }
+      uint64_t least_before = warp_scan(least_mass, lane), most_before = warp_scan(most_mass, lane);
+      const uint64_t least_all = __shfl_sync(~0u, least_before, 31), most_all = __shfl_sync(~0u, most_before, 31);
+      least_before -= least_mass, most_before -= most_mass;
+      int b0 = 0, b1 = kBins;
+      bool have1 = false;
+#pragma unroll
+      for (int i = 0; i < kPer; i++) {
+        // the mass before eighth b is between these
+        const uint64_t tail_most = most_all - most_before, tail_least = least_all - least_before;
+        const uint64_t at_most = min(most_before, all - min(all, tail_least));
+        const uint64_t at_least = max(least_before, all - min(all, tail_most));
+        const int b = lane * kPer + i;
+        if (at_most < cut) b0 = b;
+        if (at_least >= cut && !have1) b1 = b, have1 = true;
+        least_before += lo[i], most_before += hi[i];
+      }
+      eighth0 = (int)__reduce_max_sync(~0u, (uint32_t)b0);
+      eighth1 = (int)__reduce_min_sync(~0u, (uint32_t)b1);
+      eighth1 = max(eighth1, eighth0 + 1);
+    }
+    uint32_t among = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; i++)
+      if (lane * kPer + i >= eighth0 && lane * kPer + i < eighth1) among += counts[i];
+    among = __reduce_add_sync(~0u, among);
+
+    Place end;
+    uint64_t mass;
+    if (among > (uint32_t)kList) {
+      // too many to be listed (long ties, flat rows, large k): the searches go over the row
+      if (by_k) {
+        end = prefix(false, top_k, 0, kBins, &mass);
+        if (by_p) end = prefix(true, max((uint64_t)1, share(part_of(top_p), mass)), 0, kBins, &mass);
+      } else {
+        end = prefix(true, cut, 0, kBins, &mass);
+      }
+      return end;
+    }
+    // list them, add up what is before them
+    uint64_t above = 0;
+    const float t0 = eighth0 * 0.125f, t1 = eighth1 * 0.125f;
+    row_entries(fmaxf(least, -t1), [&](float d, int32_t i) {
+      if (-d < t0) above += weight(d);
+      else if (-d < t1) sh.list[atomicAdd(&sh.listed, 1u)] = make_uint2(key_of(d), (uint32_t)i);
+    });
+    above = warp_sum(above);
+    if (lane == 0) sh.above[warp] = above;
+    gather();
+    // everybody takes everybody's
+    uint32_t theirs = 0;
+    if (lane < (int)size) theirs = ld_remote32(remote(&sh.listed, lane));
+    const uint32_t ends = (uint32_t)warp_scan(theirs, lane);
+    for (uint32_t r = warp; r < size; r += W) {
+      const uint32_t have = __shfl_sync(~0u, theirs, r), at = __shfl_sync(~0u, ends, r) - have;
+      for (uint32_t i = lane; i < have; i += 32) {
+        const uint64_t v = ld_remote64(remote(&sh.list[i], r));
+        sh.all[at + i] = make_uint2((uint32_t)v, (uint32_t)(v >> 32));
+      }
+    }
+    uint64_t before = 0;
+    for (uint32_t i = lane; i < size * W; i += 32) before += ld_remote64(remote(&sh.above[i % W], i / W));
+    before = warp_sum(before);
+    listed = (int32_t)among;
+    team();
+    if (by_k) {
+      end = prefix(false, top_k, 0, eighth1, &mass);
+      if (by_p) end = prefix(true, max((uint64_t)1, share(part_of(top_p), mass)), 0, eighth1, &mass);
+    } else {
+      end = prefix(true, cut - before, eighth0, eighth1, &mass);
+      if (end.key == 0x7fffffffu) end = Place{__float_as_uint(t1), 0};
+    }
+    return end;
+  }
+};
+
+template <typename T, int W>
+__global__ __launch_bounds__(W * 32 + 32, W == 8 ? 2 : 1) void sample_kernel(const SampleArgs a) {
+  extern __shared__ uint4 buffers[];   // two buffers of a.steps steps
+  __shared__ Picks<W> sh;
+  constexpr int kE = Elem<T>::kPerVec, kLog2W = W == 16 ? 4 : 3;
+  const uint32_t size = cluster_size(), rank = cluster_rank();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t first = blockIdx.x / size, step = gridDim.x / size;
+  const uint32_t turns = ((uint32_t)a.rows - first + step - 1) / step;   // (at most one cluster a row)
+  const int log2_size = __ffs(size) - 1;
+  if (threadIdx.x == 0) {
+    for (int b = 0; b < 2; b++) {
+      bar_init(&sh.full[b], 2);
+      bar_init(&sh.empty[b], W);
+      bar_init(&sh.gate[b], size * W);
+      bar_init(&sh.told[b], 1);
+      bar_expect(&sh.told[b], size * W * 8);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  cluster_sync();   // every CTA's barriers are ready
+
+  auto row_of = [&](uint32_t it) { return (int64_t)(first + it * step); };
+  auto stream = [&](uint32_t it) {
+    Stream<T> x;
+    x.set(static_cast<const T *>(a.logits) + row_of(it) * a.stride, a.vocab, rank, log2_size, buffers + (it & 1) * a.steps * 32);
+    return x;
+  };
+  if (warp == W) {
+    bool ok = true;
+    for (uint32_t it = 0; it < turns; it++) {
+      if (it > 1) ok = __all_sync(~0u, bar_wait(&sh.empty[it & 1], ((it >> 1) - 1) & 1));
+      if (!ok) break;
+      stream(it).bring(static_cast<const T *>(a.logits) + row_of(it) * a.stride, &sh.full[it & 1]);
+    }
+  } else {
+    Picker<T, W> s(sh);
+    s.rank = rank, s.size = size;
+    const uint32_t segment = rank * W + warp;
+    uint32_t it = 0;
+    for (; it < turns; it++) {
+      const int64_t row = row_of(it);
+      s.x = stream(it);
+      s.st0 = s.x.step_of(segment, log2_size + kLog2W) - s.x.begin / 32;
+      s.st1 = s.x.step_of(segment + 1, log2_size + kLog2W) - s.x.begin / 32;
+      const float temperature = a.s.temperatures ? a.s.temperatures[row] : a.s.temperature;
+      const int32_t top_k = a.s.top_ks ? a.s.top_ks[row] : a.s.top_k;
+      const float top_p = a.s.top_ps ? a.s.top_ps[row] : a.s.top_p;
+      const float min_p = a.s.min_ps ? a.s.min_ps[row] : a.s.min_p;
+      const float u = a.u[row];
+      const bool greedy = !(temperature > 0.0f), by_k = top_k > 0 && top_k < a.vocab, by_p = top_p < 1.0f;
+      s.agree(bar_wait(&sh.full[it & 1], (it >> 1) & 1));
+      if (!s.ok) break;
+
+      // The largest number (NaN is passed over).  Beside it, for a greedy row,
+      // its first index; for top-k, the j-th largest of the threads' maxima: in
+      // half of the cluster's warps that is j entries each, k together.
+      float m = -INFINITY;
+      for (int32_t st = s.st0; st < s.st1; st++) m = Elem<T>::vec_max(s.x.buf[st * 32 + lane], m);
+      const float of_thread = m;
+      m = warp_max_all(m);
+      const uint32_t half = size * W / 2, j = ((uint32_t)top_k + half - 1) / half;
+      uint32_t beside = 0;
+      if (greedy) {
+        beside = 0xffffffffu;
+        for (int32_t st = s.st0; st < s.st1; st++) {
+          float v[kE];
+          Elem<T>::unpack(s.x.buf[st * 32 + lane], v);
+#pragma unroll
+          for (int e = 0; e < kE; e++)
+            if (v[e] == m) beside = min(beside, (uint32_t)s.x.index(st * 32 + lane, e));
+        }
+        beside = __reduce_min_sync(~0u, beside);
+      } else if (by_k) {
+        beside = ordered(-INFINITY);
+        if (j <= 32) {
+          const uint32_t mine = ordered(of_thread);
+          uint32_t place = 0;
+          for (int l = 0; l < 32; l++) {
+            const uint32_t other = __shfl_sync(~0u, mine, l);
+            place += other > mine || (other == mine && l < lane);
+          }
+          beside = __shfl_sync(~0u, mine, __ffs(__ballot_sync(~0u, place == j - 1)) - 1);
+        }
+      }
+      const uint64_t *box = s.tell(((uint64_t)beside << 32) | __float_as_uint(m));
+      if (!s.ok) break;
+      constexpr int kPer = (kMaxCluster * W + 31) / 32;
+      uint32_t besides[kPer];
+      float tops[kPer];
+#pragma unroll
+      for (int i = 0; i < kPer; i++) {
+        const bool have = i * 32 + lane < (int)(size * W);
+        const uint64_t v = have ? box[i * 32 + lane] : 0;
+        tops[i] = have ? __uint_as_float((uint32_t)v) : -INFINITY;
+        besides[i] = have ? (uint32_t)(v >> 32) : 0;
+        m = fmaxf(m, tops[i]);
+      }
+      m = warp_max_all(m);
+
+      bool draw = false;
+      if (m == -INFINITY) {   // nothing left to choose from
+        if (rank == 0 && threadIdx.x == 0) a.tokens[row] = -1, a.logps[row] = -INFINITY;
+      } else if (greedy) {
+        uint32_t best = 0xffffffffu;
+#pragma unroll
+        for (int i = 0; i < kPer; i++)
+          if (tops[i] == m) best = min(best, besides[i]);
+        best = __reduce_min_sync(~0u, best);
+        if (rank == 0 && threadIdx.x == 0) a.tokens[row] = best, a.logps[row] = 0.0f;
+      } else {
+        draw = true;
+      }
+      if (draw) {
+        s.m = m;
+        s.c = __fdiv_rn(1.44269504f, temperature);
+        s.special = !(m < INFINITY && s.c < INFINITY);
+        Place end = {0x7fffffffu, 0};
+        if (by_k || by_p) {
+          float least = kFloor;
+          if (by_k) {
+            // the largest number, in its upper 16 bits, that half of the warps' reach
+            uint32_t at = 0;
+            for (int bit = 31; bit >= 16; bit--) {
+              const uint32_t t = at | 1u << bit;
+              uint32_t reach = 0;
+#pragma unroll
+              for (int i = 0; i < kPer; i++) reach += __popc(__ballot_sync(~0u, besides[i] >= t));
+              if (reach >= half) at = t;
+            }
+            const float v = from_ordered(at);
+            if (v > -INFINITY) least = fmaxf(kFloor, v == m ? 0.0f : (v - m) * s.c);   // (fmaxf passes NaN over)
+          }
+          end = s.kept_prefix(top_k, by_p, top_p, least);
+          if (!s.ok) break;
+        }
+        const uint32_t floor_w = min_p > 0.0f ? __float2uint_rn(fminf(min_p, 1.0f) * 2147483648.0f) : 0;
+        auto kept = [&](float d, int32_t i) -> uint32_t {
+          const uint32_t q = key_of(d);
+          if (!(q < end.key || (q == end.key && i < end.index))) return 0;
+          const uint32_t w = weight(d);
+          return w >= floor_w ? w : 0;
+        };
+        // the kept mass: of this warp, before it, of the row
+        uint64_t mine = 0;
+        if (!by_k && !by_p && floor_w == 0) {
+          for (int32_t st = s.st0; st < s.st1; st++) {
+            float d[kE];
+            s.octaves(s.x.buf[st * 32 + lane], d);
+#pragma unroll
+            for (int e = 0; e < kE; e++) mine += weight(d[e]);   // 0 from kFloor on, and for NaN
+          }
+        } else {
+          s.row_entries(kFloor, [&](float d, int32_t i) { mine += kept(d, i); });
+        }
+        mine = warp_sum(mine);
+        box = s.tell(mine);
+        if (!s.ok) break;
+        uint64_t before = 0, z = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; i++)
+          if (i * 32 + lane < (int)(size * W)) {
+            const uint64_t v = box[i * 32 + lane];
+            z += v;
+            if (i * 32 + lane < (int)segment) before += v;
+          }
+        z = warp_sum(z);
+        before = warp_sum(before);
+        // the entry at which the running sum passes the target
+        const uint64_t part = u > 0.0f ? (u < 1.0f ? part_of(u) : 0xffffffffull) : 0;
+        const uint64_t target = share(part, z);
+        if (target >= before && target < before + mine) {
+          for (int32_t st = s.st0; st < s.st1; st++) {
+            const int32_t vec = st * 32 + lane;
+            float d[kE];
+            uint32_t w[kE];
+            s.octaves(s.x.buf[vec], d);
+            uint64_t of_vec = 0;
+#pragma unroll
+            for (int e = 0; e < kE; e++) {
+              w[e] = d[e] > kFloor ? kept(d[e], s.x.index(vec, e)) : 0;
+              of_vec += w[e];
+            }
+            uint64_t upto = before + warp_scan(of_vec, lane);
+            const uint64_t after = __shfl_sync(~0u, upto, 31);
+            if (target < after) {
+              upto -= of_vec;
+#pragma unroll
+              for (int e = 0; e < kE; e++) {
+                if (target >= upto && target < upto + w[e]) {
+                  a.tokens[row] = s.x.index(vec, e);
+                  a.logps[row] = (d[e] - log2f((float)z * 4.6566128730773926e-10f)) * 0.69314718f;
+                }
+                upto += w[e];
+              }
+              break;
+            }
+            before = after;
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) bar_arrive(&sh.empty[it & 1]);
+    }
+    if (!s.ok) {
+      // a wait gave up: what is not done is marked, copies in flight land before the CTA goes
+      if (rank == 0 && threadIdx.x == 0)
+        for (; it < turns; it++) a.tokens[row_of(it)] = -1, a.logps[row_of(it)] = NAN;
+      for (int b = 0; b < 2; b++)
+        for (uint32_t parity = 0; parity < 2; parity++) bar_wait(&sh.full[b], parity);
+    }
+  }
+  __syncwarp();
+  cluster_sync();
+}
+
+constexpr int kDevices = 16;   // whose occupancy is kept
+
+template <int W>
+constexpr int kMostSteps = (int)(((227 << 10) - sizeof(Picks<W>) - 1024) / (2 * 32 * 16));
+
+template <typename T, int W>
+int run_sample(SampleArgs a, int size, int log2, cudaStream_t stream) {
+  static std::atomic<int> fits[kDevices][4][kMostSteps<W> + 1];   // clusters at once, by size and steps (0: not known)
+  auto kernel = sample_kernel<T, W>;
+  constexpr int kThreads = W * 32 + 32;
+  const size_t shared = (size_t)a.steps * 2 * 32 * 16;
+  int device = 0, most = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return note_cuda(e);
+  if (device < kDevices) most = fits[device][log2][a.steps].load(std::memory_order_relaxed);
+  if (most == 0) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSteps<W> * 2 * 32 * 16);
+    if (e == cudaSuccess) e = launch_rows(kernel, a, 1, size, kThreads, shared, stream, &most);
+    if (e != cudaSuccess) return note_cuda(e);
+    if (most < 1) return SEQSUM_ECUDA;
+    if (device < kDevices) fits[device][log2][a.steps].store(most, std::memory_order_relaxed);
+  }
+  e = launch_rows(kernel, a, a.rows < most ? a.rows : most, size, kThreads, shared, stream);
   return e == cudaSuccess ? SEQSUM_OK : note_cuda(e);
 }
 
-// The smallest cluster and vectors a thread that hold a row, more CTAs where
-// the rows are few.
+// CTAs a row: enough to hold it, and as many as there is room for at once.
 template <typename T>
-int choose_sample(const SampleArgs &a, cudaStream_t stream) {
-  constexpr int NT = 512;
-  const int64_t vecs = ((int64_t)a.vocab + 2 * Elem<T>::kPerVec - 2) / Elem<T>::kPerVec;   // whatever the alignment
+int choose_sample(SampleArgs a, cudaStream_t stream) {
+  constexpr int kE = Elem<T>::kPerVec;
+  const int64_t vecs = ((int64_t)a.vocab + kE - 1) / kE + 1;   // whatever the alignment
+  const int64_t steps = (vecs + 31) / 32;
   const int sms = multiprocessors();
-  int size = 1;
-  while (size < kMaxCluster && (vecs > (int64_t)size * NT * 8 || a.rows * size * 2 <= sms)) size *= 2;
-  const int64_t per = ((vecs + size - 1) / size + NT - 1) / NT;
-  if (per <= 1) return run_sample<T, 1, NT>(a, size, stream);
-  if (per <= 2) return run_sample<T, 2, NT>(a, size, stream);
-  if (per <= 4) return run_sample<T, 4, NT>(a, size, stream);
-  if (per <= 8) return run_sample<T, 8, NT>(a, size, stream);
-  return run_sample<T, 0, NT>(a, size, stream);
+  int size = 1, log2 = 0;
+  while (size < kMaxCluster && (steps > (int64_t)size * 66 || (a.rows * size * 2 <= sms && steps > (int64_t)size * 8)))
+    size *= 2, log2++;
+  a.steps = (int32_t)((steps + size - 1) / size);
+  if (a.steps > kMostSteps<16>) {
+    const cudaError_t e = launch_rows(sample_reread_kernel<T, 512>, a, a.rows, kMaxCluster, 512, 0, stream);
+    return e == cudaSuccess ? SEQSUM_OK : note_cuda(e);
+  }
+  // (one CTA an SM from 66 steps on: then twice the warps)
+  return a.steps > 66 ? run_sample<T, 16>(a, size, log2, stream) : run_sample<T, 8>(a, size, log2, stream);
 }
 
 }  // namespace
@@ -367,7 +1027,7 @@ extern "C" int seqsum_sample_tokens(const void *logits, int32_t dtype, int64_t r
   if (rows == 0) return SEQSUM_OK;
   if (!u || !tokens || !logps || (vocab > 0 && !logits) || row_stride < 0) return SEQSUM_EINVAL;
   if (reinterpret_cast<uintptr_t>(logits) % (dtype == SEQSUM_FP32 ? 4 : 2)) return SEQSUM_EINVAL;
-  sq::SampleArgs a = {logits, rows, row_stride, (int32_t)vocab, u, *sampling, tokens, logps};
+  sq::SampleArgs a = {logits, rows, row_stride, (int32_t)vocab, u, *sampling, tokens, logps, 0};
   if (dtype == SEQSUM_FP32) return sq::choose_sample<float>(a, stream);
   if (dtype == SEQSUM_FP16) return sq::choose_sample<__half>(a, stream);
   return sq::choose_sample<__nv_bfloat16>(a, stream);
