@@ -359,15 +359,16 @@ constexpr int kList = 2048;   // entries that a search can take out of the row
 template <int W>
 struct Picks {
   static constexpr int kBoxes = kMaxCluster * W;
-  uint64_t full[2], empty[2], told[2], gate[2];
-  uint64_t box[2][kBoxes];        // a word of every warp of the cluster
+  uint64_t full[2], empty[2], told[4], gate[2];
+  uint64_t box[4][kBoxes];        // a word of every warp of the cluster
+  uint64_t step_mass[32];         // of the segment that the token is in
   uint64_t mass[W], above[W];     // of the warps' entries; of those before the listed ones
   uint32_t heads[kBins];          // entries by eighths of an octave
   uint4 bins[2][kBins];           // a split: count, and mass in two halves
   uint32_t bin_count[kBins];      // ... summed over whom it concerns
   uint64_t bin_mass[kBins];
   uint32_t listed, small_listed;
-  uint2 small[32];                // the last few entries of a search
+  uint4 small[32];                // the last few entries of a search: key, index, weight
   uint2 list[kList], all[kList];  // (key, index): this CTA's entries, the row's
 };
 
@@ -382,11 +383,12 @@ struct Picker {
   static constexpr int kE = Elem<T>::kPerVec, kThreads = W * 32;
   Picks<W> &sh;
   Stream<T> x;
-  uint32_t rank, size, told = 0, gated = 0;
+  uint32_t rank, size, posted = 0, heard = 0, gated = 0;
   int32_t st0, st1;     // this warp's steps
   float m, c;
   bool special;         // (v - m) * c needs care
-  bool ok = true;
+  bool came = true;     // no wait of this warp gave up
+  bool ok = true;       // ... none of the CTA's, as of the last agreement
   int32_t listed = -1;  // entries of sh.all, once a search goes over those; -1: over the row
 
   __device__ Picker(Picks<W> &s) : sh(s) {}
@@ -395,24 +397,28 @@ struct Picker {
 
   __device__ __forceinline__ void team() const { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kThreads) : "memory"); }
   // all of the CTA's working warps go on together or give up together
-  __device__ __forceinline__ void agree(bool mine) {
+  __device__ __forceinline__ void agree() {
     uint32_t all;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(all)
-        : "r"((uint32_t)mine), "n"(kThreads)
+        : "r"((uint32_t)came), "n"(kThreads)
         : "memory");
     ok &= all != 0;
   }
-  // every warp's word to every warp: in the box that is returned
-  __device__ __forceinline__ const uint64_t *tell(uint64_t v) {
-    const uint32_t b = told & 1, parity = (told >> 1) & 1;
-    told++;
-    const Exchange e = {sh.box[b], &sh.told[b], size * W * 8};
+  // A word of every warp to every warp.  Two may be on their way: a warp posts
+  // its word after next only once it has waited for this one, so that of four
+  // boxes the one that is written is never one that is still read.
+  __device__ __forceinline__ void post(uint64_t v) {
+    const Exchange e = {sh.box[posted & 3], &sh.told[posted & 3], size * W * 8};
+    posted++;
     e.post((int32_t)(rank * W + (threadIdx.x >> 5)), v, size);
-    const bool came = bar_wait(e.bar, parity);
-    if (threadIdx.x == 0) e.ready();
-    agree(came);
+  }
+  __device__ __forceinline__ const uint64_t *hear() {
+    const uint32_t b = heard & 3, parity = (heard >> 2) & 1;
+    heard++;
+    came &= bar_wait(&sh.told[b], parity);
+    if (threadIdx.x == 0) bar_expect(&sh.told[b], size * W * 8);
     return sh.box[b];
   }
   // what any working thread of the cluster wrote to shared memory before is seen after
@@ -421,7 +427,8 @@ struct Picker {
     const uint32_t parity = (gated >> 1) & 1;
     gated++;
     arrive_everywhere(bar, size);
-    agree(bar_wait(bar, parity));
+    came &= bar_wait(bar, parity);
+    agree();
   }
 
   // ---- entries
@@ -437,16 +444,26 @@ struct Picker {
       for (int e = 0; e < kE; e += 2) split(mul2(add2(pair(d[e], d[e + 1]), mm), cc), d[e], d[e + 1]);
     }
   }
-  // f(octaves, index) of the row's entries above `from` (at least kFloor) in this thread
+  // a logit that entries from `from` octaves on reach, with room for roundings
+  __device__ __forceinline__ float reached_from(float from) const {
+    const float v = m + __fdiv_rn(from, c) * 1.00001f, t = v - (fabsf(v) + fabsf(m)) * 1e-6f;
+    return special || !(t > -INFINITY) ? -INFINITY : t;
+  }
+  // f(octaves, index) of the row's entries from `from` octaves (at least kFloor) on in this thread
   template <typename F>
   __device__ __forceinline__ void row_entries(float from, F f) const {
     const int lane = threadIdx.x & 31;
+    const float least = reached_from(from);
+#pragma unroll 4
     for (int32_t st = st0; st < st1; st++) {
-      float d[kE];
-      octaves(x.buf[st * 32 + lane], d);
+      const uint4 w = x.buf[st * 32 + lane];
+      if (Elem<T>::vec_max(w, -INFINITY) >= least) {
+        float d[kE];
+        octaves(w, d);
 #pragma unroll
-      for (int e = 0; e < kE; e++)
-        if (d[e] >= from && d[e] > kFloor) f(d[e], x.index(st * 32 + lane, e));
+        for (int e = 0; e < kE; e++)
+          if (d[e] >= from && d[e] > kFloor) f(d[e], x.index(st * 32 + lane, e));
+      }
     }
   }
   // ... or, once there is one, of the list
@@ -591,19 +608,20 @@ struct Picker {
       const uint32_t key = key_of(d);
       if (inside(key, i)) {
         const uint32_t at = atomicAdd(&sh.small_listed, 1u);
-        if (at < 32) sh.small[at] = make_uint2(key, (uint32_t)i);
+        if (at < 32) sh.small[at] = make_uint4(key, (uint32_t)i, weight(d), 0);
       }
     });
     team();
     const uint32_t lane = threadIdx.x & 31;
     const bool have = lane < n;
-    const uint2 v = have ? sh.small[lane] : make_uint2(~0u, ~0u);
-    const uint32_t w = have ? weight(-__uint_as_float(v.x)) : 0;
+    const uint4 v = have ? sh.small[lane] : make_uint4(~0u, ~0u, 0, 0);
+    const uint32_t w = v.z;
     uint32_t count = 0;
     uint64_t sum = 0;
+#pragma unroll 8
     for (uint32_t j = 0; j < n; j++) {
-      const uint32_t kj = __shfl_sync(~0u, v.x, j), ij = __shfl_sync(~0u, v.y, j), wj = __shfl_sync(~0u, w, j);
-      if (kj < v.x || (kj == v.x && ij < v.y)) count++, sum += wj;
+      const uint4 o = sh.small[j];
+      if (o.x < v.x || (o.x == v.x && o.y < v.y)) count++, sum += o.z;
     }
     const bool last = have && (by_mass ? sum < need && need <= sum + w : count + 1 == need);
     const int o = max(0, __ffs(__ballot_sync(~0u, last)) - 1);
@@ -770,6 +788,8 @@ __global__ __launch_bounds__(W * 32 + 32, W == 8 ? 2 : 1) void sample_kernel(con
       bar_init(&sh.full[b], 2);
       bar_init(&sh.empty[b], W);
       bar_init(&sh.gate[b], size * W);
+    }
+    for (int b = 0; b < 4; b++) {
       bar_init(&sh.told[b], 1);
       bar_expect(&sh.told[b], size * W * 8);
     }
@@ -793,31 +813,31 @@ __global__ __launch_bounds__(W * 32 + 32, W == 8 ? 2 : 1) void sample_kernel(con
   } else {
     Picker<T, W> s(sh);
     s.rank = rank, s.size = size;
-    const uint32_t segment = rank * W + warp;
-    uint32_t it = 0;
-    for (; it < turns; it++) {
-      const int64_t row = row_of(it);
+    constexpr int kPer = (kMaxCluster * W + 31) / 32;
+    const uint32_t half = size * W / 2;
+    const int log2_segments = log2_size + kLog2W;
+    auto place = [&](uint32_t it) {
       s.x = stream(it);
-      s.st0 = s.x.step_of(segment, log2_size + kLog2W) - s.x.begin / 32;
-      s.st1 = s.x.step_of(segment + 1, log2_size + kLog2W) - s.x.begin / 32;
-      const float temperature = a.s.temperatures ? a.s.temperatures[row] : a.s.temperature;
-      const int32_t top_k = a.s.top_ks ? a.s.top_ks[row] : a.s.top_k;
-      const float top_p = a.s.top_ps ? a.s.top_ps[row] : a.s.top_p;
-      const float min_p = a.s.min_ps ? a.s.min_ps[row] : a.s.min_p;
-      const float u = a.u[row];
-      const bool greedy = !(temperature > 0.0f), by_k = top_k > 0 && top_k < a.vocab, by_p = top_p < 1.0f;
-      s.agree(bar_wait(&sh.full[it & 1], (it >> 1) & 1));
-      if (!s.ok) break;
+      s.st0 = s.x.step_of(rank * W + warp, log2_segments) - s.x.begin / 32;
+      s.st1 = s.x.step_of(rank * W + warp + 1, log2_segments) - s.x.begin / 32;
+    };
+    auto temperature_of = [&](int64_t row) { return a.s.temperatures ? a.s.temperatures[row] : a.s.temperature; };
+    auto top_k_of = [&](int64_t row) { return a.s.top_ks ? a.s.top_ks[row] : a.s.top_k; };
 
-      // The largest number (NaN is passed over).  Beside it, for a greedy row,
-      // its first index; for top-k, the j-th largest of the threads' maxima: in
-      // half of the cluster's warps that is j entries each, k together.
+    // A row's first part: its largest number (NaN is passed over).  Beside it,
+    // for a greedy row, its first index; for top-k, the j-th largest of the
+    // threads' maxima: j entries each in half of the cluster's warps are k.
+    auto look = [&](uint32_t it) {
+      place(it);
+      const bool greedy = !(temperature_of(row_of(it)) > 0.0f);
+      const int32_t top_k = top_k_of(row_of(it));
+      s.came &= bar_wait(&sh.full[it & 1], (it >> 1) & 1);
       float m = -INFINITY;
+#pragma unroll 4
       for (int32_t st = s.st0; st < s.st1; st++) m = Elem<T>::vec_max(s.x.buf[st * 32 + lane], m);
       const float of_thread = m;
       m = warp_max_all(m);
-      const uint32_t half = size * W / 2, j = ((uint32_t)top_k + half - 1) / half;
-      uint32_t beside = 0;
+      uint32_t beside = ordered(-INFINITY);
       if (greedy) {
         beside = 0xffffffffu;
         for (int32_t st = s.st0; st < s.st1; st++) {
@@ -828,23 +848,34 @@ __global__ __launch_bounds__(W * 32 + 32, W == 8 ? 2 : 1) void sample_kernel(con
             if (v[e] == m) beside = min(beside, (uint32_t)s.x.index(st * 32 + lane, e));
         }
         beside = __reduce_min_sync(~0u, beside);
-      } else if (by_k) {
-        beside = ordered(-INFINITY);
+      } else if (top_k > 0 && top_k < a.vocab) {
+        const uint32_t j = ((uint32_t)top_k + half - 1) / half;
         if (j <= 32) {
-          const uint32_t mine = ordered(of_thread);
-          uint32_t place = 0;
-          for (int l = 0; l < 32; l++) {
-            const uint32_t other = __shfl_sync(~0u, mine, l);
-            place += other > mine || (other == mine && l < lane);
+          uint32_t mine = ordered(of_thread);
+          beside = ordered(m);
+          for (uint32_t i = 1; i < j; i++) {   // without the largest so far, one lane of its
+            if (lane == __ffs(__ballot_sync(~0u, mine == beside)) - 1) mine = 0;
+            beside = __reduce_max_sync(~0u, mine);
           }
-          beside = __shfl_sync(~0u, mine, __ffs(__ballot_sync(~0u, place == j - 1)) - 1);
         }
       }
-      const uint64_t *box = s.tell(((uint64_t)beside << 32) | __float_as_uint(m));
-      if (!s.ok) break;
-      constexpr int kPer = (kMaxCluster * W + 31) / 32;
+      s.post(((uint64_t)beside << 32) | __float_as_uint(m));
+    };
+
+    look(0);
+    uint32_t it = 0;
+    for (; it < turns; it++) {
+      // the second part: what is kept of the row, and its mass by warps
+      const int64_t row = row_of(it);
+      if (it > 0) place(it);
+      const float temperature = temperature_of(row);
+      const int32_t top_k = top_k_of(row);
+      const float top_p = a.s.top_ps ? a.s.top_ps[row] : a.s.top_p;
+      const float min_p = a.s.min_ps ? a.s.min_ps[row] : a.s.min_p;
+      const bool greedy = !(temperature > 0.0f), by_k = top_k > 0 && top_k < a.vocab, by_p = top_p < 1.0f;
+      const uint64_t *box = s.hear();
       uint32_t besides[kPer];
-      float tops[kPer];
+      float tops[kPer], m = -INFINITY;
 #pragma unroll
       for (int i = 0; i < kPer; i++) {
         const bool have = i * 32 + lane < (int)(size * W);
@@ -854,8 +885,18 @@ __global__ __launch_bounds__(W * 32 + 32, W == 8 ? 2 : 1) void sample_kernel(con
         m = fmaxf(m, tops[i]);
       }
       m = warp_max_all(m);
+      if (by_k || by_p) s.agree();
+      if (!s.ok) break;
 
-      bool draw = false;
+      Place end = {0x7fffffffu, 0};
+      const uint32_t floor_w = min_p > 0.0f ? __float2uint_rn(fminf(min_p, 1.0f) * 2147483648.0f) : 0;
+      auto kept = [&](float d, int32_t i) -> uint32_t {
+        const uint32_t q = key_of(d);
+        if (!(q < end.key || (q == end.key && i < end.index))) return 0;
+        const uint32_t w = weight(d);
+        return w >= floor_w ? w : 0;
+      };
+      const bool draw = m > -INFINITY && !greedy;
       if (m == -INFINITY) {   // nothing left to choose from
         if (rank == 0 && threadIdx.x == 0) a.tokens[row] = -1, a.logps[row] = -INFINITY;
       } else if (greedy) {
@@ -866,95 +907,109 @@ __global__ __launch_bounds__(W * 32 + 32, W == 8 ? 2 : 1) void sample_kernel(con
         best = __reduce_min_sync(~0u, best);
         if (rank == 0 && threadIdx.x == 0) a.tokens[row] = best, a.logps[row] = 0.0f;
       } else {
-        draw = true;
-      }
-      if (draw) {
         s.m = m;
         s.c = __fdiv_rn(1.44269504f, temperature);
         s.special = !(m < INFINITY && s.c < INFINITY);
-        Place end = {0x7fffffffu, 0};
         if (by_k || by_p) {
           float least = kFloor;
           if (by_k) {
-            // the largest number, in its upper 16 bits, that half of the warps' reach
-            uint32_t at = 0;
-            for (int bit = 31; bit >= 16; bit--) {
-              const uint32_t t = at | 1u << bit;
-              uint32_t reach = 0;
-#pragma unroll
-              for (int i = 0; i < kPer; i++) reach += __popc(__ballot_sync(~0u, besides[i] >= t));
-              if (reach >= half) at = t;
-            }
-            const float v = from_ordered(at);
+            // a number that one warp of each two reaches: half of them
+            uint32_t at;
+            if (size * W <= 32) at = max(besides[0], __shfl_xor_sync(~0u, besides[0], half));
+            else if (kPer == 2 || size * W <= 64) at = max(besides[0], besides[1]);
+            else at = min(max(besides[0], besides[kPer / 2]), max(besides[1], besides[kPer - 1]));
+            if (lane >= (int)half) at = ~0u;
+            const float v = from_ordered(__reduce_min_sync(~0u, at));
             if (v > -INFINITY) least = fmaxf(kFloor, v == m ? 0.0f : (v - m) * s.c);   // (fmaxf passes NaN over)
           }
           end = s.kept_prefix(top_k, by_p, top_p, least);
           if (!s.ok) break;
         }
-        const uint32_t floor_w = min_p > 0.0f ? __float2uint_rn(fminf(min_p, 1.0f) * 2147483648.0f) : 0;
-        auto kept = [&](float d, int32_t i) -> uint32_t {
-          const uint32_t q = key_of(d);
-          if (!(q < end.key || (q == end.key && i < end.index))) return 0;
-          const uint32_t w = weight(d);
-          return w >= floor_w ? w : 0;
-        };
-        // the kept mass: of this warp, before it, of the row
         uint64_t mine = 0;
         if (!by_k && !by_p && floor_w == 0) {
+#pragma unroll 4
           for (int32_t st = s.st0; st < s.st1; st++) {
             float d[kE];
             s.octaves(s.x.buf[st * 32 + lane], d);
-#pragma unroll
-            for (int e = 0; e < kE; e++) mine += weight(d[e]);   // 0 from kFloor on, and for NaN
-          }
-        } else {
-          s.row_entries(kFloor, [&](float d, int32_t i) { mine += kept(d, i); });
-        }
-        mine = warp_sum(mine);
-        box = s.tell(mine);
-        if (!s.ok) break;
-        uint64_t before = 0, z = 0;
-#pragma unroll
-        for (int i = 0; i < kPer; i++)
-          if (i * 32 + lane < (int)(size * W)) {
-            const uint64_t v = box[i * 32 + lane];
-            z += v;
-            if (i * 32 + lane < (int)segment) before += v;
-          }
-        z = warp_sum(z);
-        before = warp_sum(before);
-        // the entry at which the running sum passes the target
-        const uint64_t part = u > 0.0f ? (u < 1.0f ? part_of(u) : 0xffffffffull) : 0;
-        const uint64_t target = share(part, z);
-        if (target >= before && target < before + mine) {
-          for (int32_t st = s.st0; st < s.st1; st++) {
-            const int32_t vec = st * 32 + lane;
-            float d[kE];
-            uint32_t w[kE];
-            s.octaves(s.x.buf[vec], d);
             uint64_t of_vec = 0;
 #pragma unroll
-            for (int e = 0; e < kE; e++) {
-              w[e] = d[e] > kFloor ? kept(d[e], s.x.index(vec, e)) : 0;
-              of_vec += w[e];
-            }
-            uint64_t upto = before + warp_scan(of_vec, lane);
-            const uint64_t after = __shfl_sync(~0u, upto, 31);
-            if (target < after) {
-              upto -= of_vec;
+            for (int e = 0; e < kE; e += 2) of_vec += (uint64_t)weight(d[e]) + weight(d[e + 1]);   // 0 from kFloor on, and for NaN
+            mine += of_vec;
+          }
+        } else {
+          s.row_entries(fmaxf(kFloor, -__uint_as_float(end.key)), [&](float d, int32_t i) { mine += kept(d, i); });
+        }
+        s.post(warp_sum(mine));
+      }
+
+      // the next row's first part, while the words of this one travel
+      if (it + 1 < turns) look(it + 1);
+
+      // the third part: the entry at which the running sum passes the target
+      if (draw) {
+        place(it);
+        const float u = a.u[row];
+        box = s.hear();
+        uint64_t upto[kPer], z = 0;
+        int owner = 0;
+        uint64_t before = 0;
 #pragma unroll
-              for (int e = 0; e < kE; e++) {
-                if (target >= upto && target < upto + w[e]) {
-                  a.tokens[row] = s.x.index(vec, e);
-                  a.logps[row] = (d[e] - log2f((float)z * 4.6566128730773926e-10f)) * 0.69314718f;
-                }
-                upto += w[e];
-              }
-              break;
-            }
-            before = after;
+        for (int i = 0; i < kPer; i++) {
+          upto[i] = z + warp_scan(i * 32 + lane < (int)(size * W) ? box[i * 32 + lane] : 0, lane);
+          z = __shfl_sync(~0u, upto[i], 31);
+        }
+        const uint64_t target = share(u > 0.0f ? (u < 1.0f ? part_of(u) : 0xffffffffull) : 0, z);
+#pragma unroll
+        for (int i = kPer - 1; i >= 0; i--) {
+          const uint32_t above = __ballot_sync(~0u, target < upto[i]);
+          if (above) {
+            owner = i * 32 + __ffs(above) - 1;
+            const uint64_t v = __shfl_sync(~0u, upto[i], __ffs(above) - 1);
+            before = v - box[owner];
           }
         }
+        s.agree();
+        if (!s.ok) break;
+        if (owner / W == (int)rank) {
+          // all of this CTA's warps take steps of that segment
+          const int32_t first_step = s.x.step_of(owner, log2_segments) - s.x.begin / 32,
+                        steps = s.x.step_of(owner + 1, log2_segments) - s.x.begin / 32 - first_step;
+          auto weights = [&](int32_t st, float *d, uint32_t *w) {
+            s.octaves(s.x.buf[(first_step + st) * 32 + lane], d);
+            uint64_t sum = 0;
+#pragma unroll
+            for (int e = 0; e < kE; e++) {
+              w[e] = d[e] > kFloor ? kept(d[e], s.x.index((first_step + st) * 32 + lane, e)) : 0;
+              sum += w[e];
+            }
+            return sum;
+          };
+          float d[kE];
+          uint32_t w[kE];
+          for (int32_t st = warp; st < steps; st += W) {
+            const uint64_t sum = warp_sum(weights(st, d, w));
+            if (lane == 0) sh.step_mass[st] = sum;
+          }
+          s.team();
+          const uint64_t of_step = lane < steps ? sh.step_mass[lane] : 0, upto_step = before + warp_scan(of_step, lane);
+          const int32_t st = __ffs(__ballot_sync(~0u, target < upto_step)) - 1;
+          if (st % W == warp) {
+            before = __shfl_sync(~0u, upto_step - of_step, st);
+            const uint64_t of_vec = weights(st, d, w);
+            uint64_t sum = before + warp_scan(of_vec, lane) - of_vec;
+#pragma unroll
+            for (int e = 0; e < kE; e++) {
+              if (target >= sum && target < sum + w[e]) {
+                a.tokens[row] = s.x.index((first_step + st) * 32 + lane, e);
+                a.logps[row] = (d[e] - log2f((float)z * 4.6566128730773926e-10f)) * 0.69314718f;
+              }
+              sum += w[e];
+            }
+          }
+        }
+      } else {
+        s.agree();
+        if (!s.ok) break;
       }
       __syncwarp();
       if (lane == 0) bar_arrive(&sh.empty[it & 1]);
