@@ -176,9 +176,25 @@ __device__ __forceinline__ float warp_max(float v) {
   for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, o));
   return v;
 }
-__device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
+__device__ __forceinline__ uint64_t warp_sum(uint64_t v) {   // of values below 2^58
+  const uint32_t lo = __reduce_add_sync(~0u, (uint32_t)v & 0x3ffffffu), mid = __reduce_add_sync(~0u, (uint32_t)(v >> 26) & 0x3ffffffu),
+                 hi = __reduce_add_sync(~0u, (uint32_t)(v >> 52));
+  return lo + ((uint64_t)mid << 26) + ((uint64_t)hi << 52);
+}
+__device__ __forceinline__ uint32_t warp_scan(uint32_t v, int lane) {   // inclusive
 #pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t u = __shfl_up_sync(~0u, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+__device__ __forceinline__ uint64_t warp_scan(uint64_t v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t u = __shfl_up_sync(~0u, v, o);
+    if (lane >= o) v += u;
+  }
   return v;
 }
 // floats as unsigned integers of the same order, and back
@@ -191,14 +207,6 @@ __device__ __forceinline__ float warp_max_all(float v) { return from_ordered(__r
 __device__ __forceinline__ float warp_add(float v) {   // the same tree in every lane
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
-  return v;
-}
-__device__ __forceinline__ uint64_t warp_scan(uint64_t v, int lane) {   // inclusive
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint64_t u = __shfl_up_sync(~0u, v, o);
-    if (lane >= o) v += u;
-  }
   return v;
 }
 

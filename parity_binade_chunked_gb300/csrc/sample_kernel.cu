@@ -389,6 +389,7 @@ struct Picker {
   bool special;         // (v - m) * c needs care
   bool came = true;     // no wait of this warp gave up
   bool ok = true;       // ... none of the CTA's, as of the last agreement
+  int lists = 0;        // made for this row
   int32_t listed = -1;  // entries of sh.all, once a search goes over those; -1: over the row
 
   __device__ Picker(Picks<W> &s) : sh(s) {}
@@ -519,32 +520,25 @@ struct Picker {
     // every warp for itself: lane l has bins 8 l to 8 l + 7
     constexpr int kPer = kBins / 32;
     const int lane = threadIdx.x & 31;
-    uint64_t n = 0, w = 0;
+    uint32_t n = 0;
+    uint64_t w = 0;
 #pragma unroll
     for (int i = 0; i < kPer; i++) n += sh.bin_count[lane * kPer + i], w += sh.bin_mass[lane * kPer + i];
-    const uint64_t v = by_mass ? w : n, upto = warp_scan(v, lane);
-    const uint32_t owner = __ballot_sync(~0u, upto - v < need && need <= upto);
-    Found f;
-    f.bin = -1;
-    uint64_t nb = warp_scan(n, lane) - n, wb = warp_scan(w, lane) - w;
-    if (owner == 0) {
-      f.count = f.count_before = 0;
-      f.mass = 0, f.mass_before = __shfl_sync(~0u, wb + w, 31);
-    } else {
-      int b = lane * kPer;
-      uint32_t bn = 0;
-      uint64_t bw = 0;
-      if (owner >> lane & 1) {
-        for (;; b++) {
-          bn = sh.bin_count[b], bw = sh.bin_mass[b];
-          if ((by_mass ? wb + bw : nb + bn) >= need) break;
-          nb += bn, wb += bw;
-        }
+    const uint64_t upto = by_mass ? warp_scan(w, lane) : warp_scan(n, lane);
+    const uint32_t reached = __ballot_sync(~0u, need <= upto);
+    const int o = reached ? __ffs(reached) - 1 : 32;   // the lane whose bins reach it
+    uint32_t nb = __reduce_add_sync(~0u, lane < o ? n : 0);
+    uint64_t wb = warp_sum(lane < o ? w : 0);
+    Found f = {-1, 0, 0, 0, wb};
+    if (o < 32) {
+      // (every lane goes through that lane's bins)
+      f.bin = o * kPer;
+      for (;; f.bin++) {
+        f.count = sh.bin_count[f.bin], f.mass = sh.bin_mass[f.bin];
+        if ((by_mass ? wb + f.mass : (uint64_t)nb + f.count) >= need) break;
+        nb += f.count, wb += f.mass;
       }
-      const int o = __ffs(owner) - 1;
-      f.bin = __shfl_sync(~0u, b, o);
-      f.count = __shfl_sync(~0u, bn, o), f.count_before = __shfl_sync(~0u, (uint32_t)nb, o);
-      f.mass = __shfl_sync(~0u, bw, o), f.mass_before = __shfl_sync(~0u, wb, o);
+      f.count_before = nb, f.mass_before = wb;
     }
     team();   // the sums may be written again
     return f;
@@ -579,6 +573,10 @@ struct Picker {
         return ties ? Place{lo, ihi} : Place{hi, 0};
       }
       auto inside = [&](uint32_t key, int32_t i) { return ties ? key == lo && i >= ilo && i < ihi : key >= lo && key < hi; };
+      if (listed < 0 && f.count <= (uint32_t)kList) {   // few enough now
+        list(__uint_as_float(lo), __uint_as_float(hi), inside);
+        if (!ok) break;
+      }
       if (listed >= 0 && f.count <= 32) return last_few(by_mass, need, before, f.count, inside, mass);
       // split keys [lo, hi), or, where that is one key, its indices [ilo, ihi)
       const uint32_t width = ties ? (uint32_t)(ihi - ilo) : hi - lo;
@@ -631,17 +629,73 @@ struct Picker {
     return p;
   }
 
+  // ---- lists
+
+  // Lists the row's entries at -d in [t0, t1) that are `inside`, every CTA all
+  // of them; returns the mass of those at -d below t0.  More than kList of
+  // them: `listed` stays -1.
+  template <typename I>
+  __device__ uint64_t list(float t0, float t1, I inside, bool want_above = false) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (lists++ > 0) gather();   // nobody still reads this row's list before
+    if (threadIdx.x == 0) sh.listed = 0;
+    team();
+    uint64_t above = 0;
+    row_entries(fmaxf(kFloor, -t1), [&](float d, int32_t i) {
+      const uint32_t key = key_of(d);
+      if (-d < t0) {
+        if (want_above) above += weight(d);
+      } else if (-d < t1 && inside(key, i)) {
+        const uint32_t at = atomicAdd(&sh.listed, 1u);
+        if (at < (uint32_t)kList) sh.list[at] = make_uint2(key, (uint32_t)i);
+      }
+    });
+    above = warp_sum(above);
+    if (lane == 0) sh.above[warp] = above;
+    gather();
+    const uint32_t theirs = lane < (int)size ? ld_remote32(remote(&sh.listed, lane)) : 0;
+    uint64_t before = 0;
+    for (uint32_t i = lane; i < size * W; i += 32) before += ld_remote64(remote(&sh.above[i % W], i / W));
+    before = warp_sum(before);
+    const uint32_t ends = warp_scan(theirs, lane), total = __shfl_sync(~0u, ends, 31);
+    if (total <= (uint32_t)kList) {
+      listed = (int32_t)total;
+      for (uint32_t r = warp; r < size; r += W) {
+        const uint32_t have = __shfl_sync(~0u, theirs, r), at = __shfl_sync(~0u, ends, r) - have;
+        for (uint32_t i = lane; i < have; i += 32) {
+          const uint64_t v = ld_remote64(remote(&sh.list[i], r));
+          sh.all[at + i] = make_uint2((uint32_t)v, (uint32_t)(v >> 32));
+        }
+      }
+    }
+    team();
+    return before;
+  }
+
   // ---- the kept prefix
 
   // Where the prefix that top-k and top-p keep ends.  `least` is a lower bound
   // of the k-th largest entry's octaves.
   __device__ Place kept_prefix(int32_t top_k, bool by_p, float top_p, float least) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int kPer = kBins / 32;
     bool by_k = top_k > 0 && top_k < x.vocab;
+    auto any = [](uint32_t, int32_t) { return true; };
+    uint64_t mass = 0;
     listed = -1;
+    lists = 0;
+    if (by_k && least > kFloor) {
+      // not many more than k entries as a rule: all of them at once
+      const int eighth1 = min(kBins, (int)(-least * 8.0f) + 1);
+      list(0.0f, eighth1 * 0.125f, any);
+      if (listed >= 0 || !ok) {
+        Place end = prefix(false, top_k, 0, eighth1, &mass);
+        if (by_p) end = prefix(true, max((uint64_t)1, share(part_of(top_p), mass)), 0, eighth1, &mass);
+        return end;
+      }
+    }
     // counts by eighths of octaves, and the mass of all that may be kept
     if (threadIdx.x < kBins) sh.heads[threadIdx.x] = 0;
-    if (threadIdx.x == 0) sh.listed = 0;
     team();
     uint64_t mine = 0;
     row_entries(least, [&](float d, int32_t) {
@@ -658,118 +712,58 @@ struct Picker {
     }
     uint64_t all = 0;
     for (uint32_t i = lane; i < size * W; i += 32) all += ld_remote64(remote(&sh.mass[i % W], i / W));
-    all = warp_sum(all);
+    all = max((uint64_t)1, warp_sum(all));
     team();
-    constexpr int kPer = kBins / 32;
     uint32_t counts[kPer], n = 0;
 #pragma unroll
     for (int i = 0; i < kPer; i++) n += counts[i] = sh.bin_count[lane * kPer + i];
-    const uint32_t upto = (uint32_t)warp_scan(n, lane), total = __shfl_sync(~0u, upto, 31);
+    const uint32_t upto = warp_scan(n, lane), total = __shfl_sync(~0u, upto, 31);
     if (by_k && total < (uint32_t)top_k) by_k = false;   // all that weighs anything is among the first k
     if (!by_k && !by_p) return Place{0x7fffffffu, 0};
 
-    // the eighths that the search has to look at
-    int eighth0 = 0, eighth1 = kBins;
-    uint64_t cut = 0;
     if (by_k) {
-      uint32_t before = upto - n;
-      int b = kBins;
-#pragma unroll
-      for (int i = kPer - 1; i >= 0; i--) {
-        // from the last bin of the lane to the first: the first whose count reaches k
-        uint32_t to = before;
-#pragma unroll
-        for (int j = 0; j <= i; j++) to += counts[j];
-        if (to >= (uint32_t)top_k) b = lane * kPer + i + 1;
-      }
-      eighth1 = __reduce_min_sync(~0u, (uint32_t)b);
-    } else {
-      if (all == 0) all = 1;
-      cut = max((uint64_t)1, share(part_of(top_p), all));
-      // Bounds of the mass before each eighth, from the counts: from its front
-      // and, what is narrower in the tail, from its back.
-      uint64_t least_mass = 0, most_mass = 0;
-      uint64_t lo[kPer], hi[kPer];
-#pragma unroll
-      for (int i = 0; i < kPer; i++) {
-        const int b = lane * kPer + i;
-        const float top = ex2(31.0f - b * 0.125f);
-        const uint64_t w1 = (uint64_t)(top * 1.00001f) + 2, w0 = (uint64_t)fmaxf(top * (0.9170040f * 0.99999f) - 2.0f, 0.0f);
-        lo[i] = counts[i] * w0, hi[i] = counts[i] * w1;
-        least_mass += lo[i], most_mass += hi[i];
-      }
-      uint64_t least_before = warp_scan(least_mass, lane), most_before = warp_scan(most_mass, lane);
-      const uint64_t least_all = __shfl_sync(~0u, least_before, 31), most_all = __shfl_sync(~0u, most_before, 31);
-      least_before -= least_mass, most_before -= most_mass;
-      int b0 = 0, b1 = kBins;
-      bool have1 = false;
-#pragma unroll
-      for (int i = 0; i < kPer; i++) {
-        // the mass before eighth b is between these
-        const uint64_t tail_most = most_all - most_before, tail_least = least_all - least_before;
-        const uint64_t at_most = min(most_before, all - min(all, tail_least));
-        const uint64_t at_least = max(least_before, all - min(all, tail_most));
-        const int b = lane * kPer + i;
-        if (at_most < cut) b0 = b;
-        if (at_least >= cut && !have1) b1 = b, have1 = true;
-        least_before += lo[i], most_before += hi[i];
-      }
-      eighth0 = (int)__reduce_max_sync(~0u, (uint32_t)b0);
-      eighth1 = (int)__reduce_min_sync(~0u, (uint32_t)b1);
-      eighth1 = max(eighth1, eighth0 + 1);
-    }
-    uint32_t among = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; i++)
-      if (lane * kPer + i >= eighth0 && lane * kPer + i < eighth1) among += counts[i];
-    among = __reduce_add_sync(~0u, among);
-
-    Place end;
-    uint64_t mass;
-    if (among > (uint32_t)kList) {
-      // too many to be listed (long ties, flat rows, large k): the searches go over the row
-      if (by_k) {
-        end = prefix(false, top_k, 0, kBins, &mass);
-        if (by_p) end = prefix(true, max((uint64_t)1, share(part_of(top_p), mass)), 0, kBins, &mass);
-      } else {
-        end = prefix(true, cut, 0, kBins, &mass);
+      // the eighth in which the count reaches k
+      const int o = __ffs(__ballot_sync(~0u, upto >= (uint32_t)top_k)) - 1;
+      uint32_t before = __shfl_sync(~0u, upto - n, o);
+      int b = o * kPer;
+      while (before + sh.bin_count[b] < (uint32_t)top_k) before += sh.bin_count[b++];
+      const uint64_t above = list(b * 0.125f, (b + 1) * 0.125f, any, true);
+      Place end = prefix(false, (uint32_t)top_k - before, b, b + 1, &mass);
+      if (by_p) {
+        listed = -1;
+        end = prefix(true, max((uint64_t)1, share(part_of(top_p), above + mass)), 0, b + 1, &mass);
       }
       return end;
     }
-    // list them, add up what is before them
-    uint64_t above = 0;
-    const float t0 = eighth0 * 0.125f, t1 = eighth1 * 0.125f;
-    row_entries(fmaxf(least, -t1), [&](float d, int32_t i) {
-      if (-d < t0) above += weight(d);
-      else if (-d < t1) sh.list[atomicAdd(&sh.listed, 1u)] = make_uint2(key_of(d), (uint32_t)i);
-    });
-    above = warp_sum(above);
-    if (lane == 0) sh.above[warp] = above;
-    gather();
-    // everybody takes everybody's
-    uint32_t theirs = 0;
-    if (lane < (int)size) theirs = ld_remote32(remote(&sh.listed, lane));
-    const uint32_t ends = (uint32_t)warp_scan(theirs, lane);
-    for (uint32_t r = warp; r < size; r += W) {
-      const uint32_t have = __shfl_sync(~0u, theirs, r), at = __shfl_sync(~0u, ends, r) - have;
-      for (uint32_t i = lane; i < have; i += 32) {
-        const uint64_t v = ld_remote64(remote(&sh.list[i], r));
-        sh.all[at + i] = make_uint2((uint32_t)v, (uint32_t)(v >> 32));
-      }
+    // The eighths that the cut can be in: bounds of the mass before each, from
+    // the counts, from the front and, narrower in the tail, from the back.
+    const uint64_t cut = max((uint64_t)1, share(part_of(top_p), all));
+    uint64_t lo[kPer], hi[kPer], least_mass = 0, most_mass = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; i++) {
+      const float top = ex2(31.0f - (lane * kPer + i) * 0.125f);   // 2^(-1/8) = 0.9170040...
+      lo[i] = counts[i] * (uint64_t)fmaxf(top * (0.9170040f * 0.99999f) - 2.0f, 0.0f);
+      hi[i] = counts[i] * ((uint64_t)(top * 1.00001f) + 2);
+      least_mass += lo[i], most_mass += hi[i];
     }
-    uint64_t before = 0;
-    for (uint32_t i = lane; i < size * W; i += 32) before += ld_remote64(remote(&sh.above[i % W], i / W));
-    before = warp_sum(before);
-    listed = (int32_t)among;
-    team();
-    if (by_k) {
-      end = prefix(false, top_k, 0, eighth1, &mass);
-      if (by_p) end = prefix(true, max((uint64_t)1, share(part_of(top_p), mass)), 0, eighth1, &mass);
-    } else {
-      end = prefix(true, cut - before, eighth0, eighth1, &mass);
-      if (end.key == 0x7fffffffu) end = Place{__float_as_uint(t1), 0};
+    uint64_t least_before = warp_scan(least_mass, lane), most_before = warp_scan(most_mass, lane);
+    const uint64_t least_all = __shfl_sync(~0u, least_before, 31), most_all = __shfl_sync(~0u, most_before, 31);
+    least_before -= least_mass, most_before -= most_mass;
+    int b0 = 0, b1 = kBins;
+#pragma unroll
+    for (int i = 0; i < kPer; i++) {
+      const uint64_t at_most = min(most_before, all - min(all, least_all - least_before));
+      const uint64_t at_least = max(least_before, all - min(all, most_all - most_before));
+      if (at_most < cut) b0 = lane * kPer + i;
+      if (at_least >= cut) b1 = min(b1, lane * kPer + i);
+      least_before += lo[i], most_before += hi[i];
     }
-    return end;
+    const int eighth0 = (int)__reduce_max_sync(~0u, (uint32_t)b0);
+    const int eighth1 = max((int)__reduce_min_sync(~0u, (uint32_t)b1), eighth0 + 1);
+    const float t1 = eighth1 * 0.125f;
+    const uint64_t above = list(eighth0 * 0.125f, t1, any, true);
+    const Place end = prefix(true, cut - above, eighth0, eighth1, &mass);
+    return end.key == 0x7fffffffu ? Place{__float_as_uint(t1), 0} : end;
   }
 };
 
