@@ -354,7 +354,8 @@ __global__ __launch_bounds__(NT) void sample_reread_kernel(const SampleArgs a) {
 
 // ---- rows streamed through shared memory (see Stream)
 
-constexpr int kList = 2048;   // entries that a search can take out of the row
+constexpr int kList = 1280;   // entries that a search can take out of the row
+constexpr int kOwn = 192;     // ... that a warp can of its segment
 
 template <int W>
 struct Picks {
@@ -370,6 +371,7 @@ struct Picks {
   uint32_t listed, small_listed;
   uint4 small[32];                // the last few entries of a search: key, index, weight
   uint2 list[kList], all[kList];  // (key, index): this CTA's entries, the row's
+  uint2 own[W][kOwn];             // a warp's
 };
 
 struct Found {
@@ -390,6 +392,8 @@ struct Picker {
   bool came = true;     // no wait of this warp gave up
   bool ok = true;       // ... none of the CTA's, as of the last agreement
   int lists = 0;        // made for this row
+  int own = -1;         // entries that this warp took out of its segment, from own_from octaves on
+  float own_from = 0.0f;
   int32_t listed = -1;  // entries of sh.all, once a search goes over those; -1: over the row
 
   __device__ Picker(Picks<W> &s) : sh(s) {}
@@ -432,6 +436,13 @@ struct Picker {
     agree();
   }
 
+  // The sum of all warps' words in a shared table of each CTA.
+  __device__ __forceinline__ uint64_t of_all(const uint64_t *table) const {
+    uint64_t v = 0;
+    for (uint32_t i = threadIdx.x & 31; i < size * W; i += 32) v += ld_remote64(remote(&table[i % W], i / W));
+    return warp_sum(v);
+  }
+
   // ---- entries
 
   __device__ __forceinline__ void octaves(uint4 w, float *d) const {
@@ -450,10 +461,43 @@ struct Picker {
     const float v = m + __fdiv_rn(from, c) * 1.00001f, t = v - (fabsf(v) + fabsf(m)) * 1e-6f;
     return special || !(t > -INFINITY) ? -INFINITY : t;
   }
+  // Takes the entries from `from` octaves on out of the warp's segment, if they
+  // are few enough: passes over them are short then, whatever their places.
+  __device__ __forceinline__ void collect(float from) {
+    const int lane = threadIdx.x & 31;
+    const float least = reached_from(from);
+    uint2 *to = sh.own[threadIdx.x >> 5];
+    int n = 0;
+    for (int32_t st = st0; st < st1 && n <= kOwn; st++) {
+      const uint4 w = x.buf[st * 32 + lane];
+      if (!__any_sync(~0u, Elem<T>::vec_max(w, -INFINITY) >= least)) continue;
+      float d[kE];
+      octaves(w, d);
+#pragma unroll
+      for (int e = 0; e < kE; e++) {
+        const bool in = d[e] >= from && d[e] > kFloor;
+        const uint32_t who = __ballot_sync(~0u, in);
+        const int at = n + __popc(who & ((1u << lane) - 1));
+        if (in && at < kOwn) to[at] = make_uint2(key_of(d[e]), (uint32_t)x.index(st * 32 + lane, e));
+        n += __popc(who);
+      }
+    }
+    __syncwarp();
+    own = n <= kOwn ? n : -1;
+    own_from = from;
+  }
   // f(octaves, index) of the row's entries from `from` octaves (at least kFloor) on in this thread
   template <typename F>
   __device__ __forceinline__ void row_entries(float from, F f) const {
     const int lane = threadIdx.x & 31;
+    if (own >= 0 && from >= own_from) {
+      for (int i = lane; i < own; i += 32) {
+        const uint2 v = sh.own[threadIdx.x >> 5][i];
+        const float d = -__uint_as_float(v.x);
+        if (d >= from) f(d, (int32_t)v.y);
+      }
+      return;
+    }
     const float least = reached_from(from);
 #pragma unroll 4
     for (int32_t st = st0; st < st1; st++) {
@@ -489,18 +533,31 @@ struct Picker {
     atomicAdd(&bins[bin].z, w >> 16);
   }
   // Entries by bin_of(key, index), where that is below kBins, and the first
-  // bin at which their count (or mass) reaches `need`.
+  // bin at which their count (or mass) reaches `need`.  With `from` above
+  // kFloor (over the row, by mass) only entries from there on are looked at,
+  // and those that bin_of puts into kBefore come before all bins.
+  static constexpr uint32_t kBefore = ~0u;
   template <typename B>
-  __device__ Found find(bool by_mass, uint64_t need, B bin_of) {
+  __device__ Found find(bool by_mass, uint64_t need, B bin_of, float from = kFloor) {
     uint4 *bins = sh.bins[gated & 1];   // (in turn: others of the cluster may still read the last one)
     if (threadIdx.x < kBins) bins[threadIdx.x] = make_uint4(0, 0, 0, 0);
     team();
-    entries([&](float d, int32_t i) {
+    uint64_t front = 0;
+    auto take = [&](float d, int32_t i) {
       const uint32_t b = bin_of(key_of(d), i);
       if (b < (uint32_t)kBins) put(bins, b, d);
-    });
+      else if (b == kBefore) front += weight(d);
+    };
+    if (from > kFloor) {
+      row_entries(from, take);
+      front = warp_sum(front);
+      if ((threadIdx.x & 31) == 0) sh.above[threadIdx.x >> 5] = front;
+    } else {
+      entries(take);
+    }
     if (listed < 0) gather();
     else team();
+    front = from > kFloor ? of_all(sh.above) : 0;
     if (threadIdx.x < kBins) {
       uint32_t n = 0;
       uint64_t w = 0;
@@ -524,12 +581,13 @@ struct Picker {
     uint64_t w = 0;
 #pragma unroll
     for (int i = 0; i < kPer; i++) n += sh.bin_count[lane * kPer + i], w += sh.bin_mass[lane * kPer + i];
-    const uint64_t upto = by_mass ? warp_scan(w, lane) : warp_scan(n, lane);
+    const uint64_t upto = by_mass ? front + warp_scan(w, lane) : warp_scan(n, lane);
     const uint32_t reached = __ballot_sync(~0u, need <= upto);
     const int o = reached ? __ffs(reached) - 1 : 32;   // the lane whose bins reach it
     uint32_t nb = __reduce_add_sync(~0u, lane < o ? n : 0);
-    uint64_t wb = warp_sum(lane < o ? w : 0);
+    uint64_t wb = front + warp_sum(lane < o ? w : 0);
     Found f = {-1, 0, 0, 0, wb};
+    if (front >= need) return team(), f;   // reached before all bins
     if (o < 32) {
       // (every lane goes through that lane's bins)
       f.bin = o * kPer;
@@ -548,20 +606,30 @@ struct Picker {
   // entries (or `need` of mass), and its mass; without one the end of all.
   // The entries' eighths of octaves lie in [eighth0, eighth1).
   __device__ Place prefix(bool by_mass, uint64_t need, int eighth0, int eighth1, uint64_t *mass) {
-    // The first split is even in octaves: by a power of two, from an eighth, so
-    // that differences and products are exact and each bin is a range of keys.
-    float scale = 8.0f;
-    for (int n = eighth1 - eighth0; n <= kBins / 2; n *= 2) scale *= 2.0f;
+    float scale;
     const float from = eighth0 * 0.125f;
-    uint32_t lo = __float_as_uint(from), hi = __float_as_uint(eighth1 * 0.125f);
-    Found f = find(by_mass, need, [&](uint32_t key, int32_t) {
-      return key >= lo && key < hi ? (uint32_t)((__uint_as_float(key) - from) * scale) : (uint32_t)kBins;
-    });
+    const Found f = find(by_mass, need, even_split(eighth0, eighth1, scale));
     if (f.bin < 0) {
       *mass = f.mass_before;
       return Place{0x7fffffffu, 0};
     }
-    lo = __float_as_uint(from + f.bin / scale), hi = __float_as_uint(from + (f.bin + 1) / scale);
+    return narrow(by_mass, need, f, __float_as_uint(from + f.bin / scale), __float_as_uint(from + (f.bin + 1) / scale), mass);
+  }
+
+  // The first split is even in octaves: by a power of two, from an eighth, so
+  // that differences and products are exact and each bin is a range of keys.
+  __device__ __forceinline__ static auto even_split(int eighth0, int eighth1, float &scale) {
+    scale = 8.0f;
+    for (int n = eighth1 - eighth0; n <= kBins / 2; n *= 2) scale *= 2.0f;
+    const float from = eighth0 * 0.125f, by = scale;
+    const uint32_t lo = __float_as_uint(from), hi = __float_as_uint(eighth1 * 0.125f);
+    return [=](uint32_t key, int32_t) {
+      return key < lo ? kBefore : key < hi ? (uint32_t)((__uint_as_float(key) - from) * by) : (uint32_t)kBins;
+    };
+  }
+
+  // ... from the bin `f` of keys [lo, hi) on.
+  __device__ Place narrow(bool by_mass, uint64_t need, Found f, uint32_t lo, uint32_t hi, uint64_t *mass) {
     int32_t ilo = 0, ihi = x.vocab;
     uint64_t before = 0;
     while (ok) {
@@ -650,13 +718,13 @@ struct Picker {
         if (at < (uint32_t)kList) sh.list[at] = make_uint2(key, (uint32_t)i);
       }
     });
-    above = warp_sum(above);
-    if (lane == 0) sh.above[warp] = above;
+    if (want_above) {
+      above = warp_sum(above);
+      if (lane == 0) sh.above[warp] = above;
+    }
     gather();
     const uint32_t theirs = lane < (int)size ? ld_remote32(remote(&sh.listed, lane)) : 0;
-    uint64_t before = 0;
-    for (uint32_t i = lane; i < size * W; i += 32) before += ld_remote64(remote(&sh.above[i % W], i / W));
-    before = warp_sum(before);
+    const uint64_t before = want_above ? of_all(sh.above) : 0;
     const uint32_t ends = warp_scan(theirs, lane), total = __shfl_sync(~0u, ends, 31);
     if (total <= (uint32_t)kList) {
       listed = (int32_t)total;
@@ -694,9 +762,73 @@ struct Picker {
         return end;
       }
     }
-    // counts by eighths of octaves, and the mass of all that may be kept
     if (threadIdx.x < kBins) sh.heads[threadIdx.x] = 0;
     team();
+    if (!by_k) {
+      // The mass of all, exactly, and every kE-th entry's eighth: the mass of
+      // the tail by eighths, nearly, and so the eighths that the cut is in.
+      // That they hold it shows when their entries are summed; if they do not,
+      // the counts below are exact.
+      uint64_t mine = 0;
+#pragma unroll 2
+      for (int32_t st = st0; st < st1; st++) {
+        float d[kE];
+        octaves(x.buf[st * 32 + lane], d);
+        uint64_t of_vec = 0;
+#pragma unroll
+        for (int e = 0; e < kE; e += 2) of_vec += (uint64_t)weight(d[e]) + weight(d[e + 1]);
+        mine += of_vec;
+        if (d[0] > kFloor) atomicAdd(&sh.heads[(int)(-d[0] * 8.0f)], 1u);
+      }
+      mine = warp_sum(mine);
+      if (lane == 0) sh.mass[warp] = mine;
+      gather();
+      if (threadIdx.x < kBins) {
+        uint32_t n = 0;
+        for (uint32_t r = 0; r < size; r++) n += ld_remote32(remote(&sh.heads[threadIdx.x], r));
+        sh.bin_count[threadIdx.x] = n;
+      }
+      const uint64_t all = max((uint64_t)1, of_all(sh.mass));
+      const uint64_t cut = max((uint64_t)1, share(part_of(top_p), all));
+      team();
+      // the tail from each eighth on: its mass and that of its squares, from the back
+      auto middle = [&](int i) { return ex2(30.9375f - (lane * kPer + i) * 0.125f); };
+      float w[kPer], tail = 0.0f, tail2 = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kPer; i++) {
+        w[i] = (float)sh.bin_count[lane * kPer + i] * (middle(i) * kE);
+        tail += w[i], tail2 += w[i] * (middle(i) * kE);
+      }
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float u = __shfl_down_sync(~0u, tail, o), u2 = __shfl_down_sync(~0u, tail2, o);
+        if (lane + o < 32) tail += u, tail2 += u2;
+      }
+      tail = __shfl_down_sync(~0u, tail, 1), tail2 = __shfl_down_sync(~0u, tail2, 1);   // after the lane's bins
+      if (lane == 31) tail = tail2 = 0.0f;
+      const float left = (float)(all - cut);   // of mass, after the cut
+      int b0 = 0, b1 = kBins;
+#pragma unroll
+      for (int i = kPer - 1; i >= 0; i--) {
+        tail += w[i], tail2 += w[i] * (middle(i) * kE);
+        const float off = 0.05f * tail + 4.0f * sqrtf(tail2);
+        if (tail - off > left) b0 = max(b0, lane * kPer + i);
+        if (tail + off <= left) b1 = lane * kPer + i;
+      }
+      const int eighth0 = (int)__reduce_max_sync(~0u, (uint32_t)b0);
+      const int eighth1 = max((int)__reduce_min_sync(~0u, (uint32_t)b1), eighth0 + 1);
+      float scale;
+      const float from = eighth0 * 0.125f;
+      const auto bins = even_split(eighth0, eighth1, scale);
+      const float least1 = fmaxf(-eighth1 * 0.125f, kFloor + 1e-5f);
+      collect(least1);
+      const Found f = find(true, cut, bins, least1);
+      if (f.bin >= 0 || !ok)
+        return narrow(true, cut, f, __float_as_uint(from + f.bin / scale), __float_as_uint(from + (f.bin + 1) / scale), &mass);
+      if (threadIdx.x < kBins) sh.heads[threadIdx.x] = 0;   // (all have read them: they have met since)
+      team();
+    }
+    // counts by eighths of octaves, and the mass of all that may be kept
     uint64_t mine = 0;
     row_entries(least, [&](float d, int32_t) {
       atomicAdd(&sh.heads[(int)(-d * 8.0f)], 1u);
@@ -710,9 +842,7 @@ struct Picker {
       for (uint32_t r = 0; r < size; r++) n += ld_remote32(remote(&sh.heads[threadIdx.x], r));
       sh.bin_count[threadIdx.x] = n;
     }
-    uint64_t all = 0;
-    for (uint32_t i = lane; i < size * W; i += 32) all += ld_remote64(remote(&sh.mass[i % W], i / W));
-    all = max((uint64_t)1, warp_sum(all));
+    const uint64_t all = max((uint64_t)1, of_all(sh.mass));
     team();
     uint32_t counts[kPer], n = 0;
 #pragma unroll
@@ -769,8 +899,8 @@ struct Picker {
 
 template <typename T, int W>
 __global__ __launch_bounds__(W * 32 + 32, W == 8 ? 2 : 1) void sample_kernel(const SampleArgs a) {
-  extern __shared__ uint4 buffers[];   // two buffers of a.steps steps
-  __shared__ Picks<W> sh;
+  extern __shared__ uint4 buffers[];   // two buffers of a.steps steps, and the rest
+  Picks<W> &sh = *reinterpret_cast<Picks<W> *>(buffers + 2 * a.steps * 32);
   constexpr int kE = Elem<T>::kPerVec, kLog2W = W == 16 ? 4 : 3;
   const uint32_t size = cluster_size(), rank = cluster_rank();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -867,6 +997,7 @@ __global__ __launch_bounds__(W * 32 + 32, W == 8 ? 2 : 1) void sample_kernel(con
       const float top_p = a.s.top_ps ? a.s.top_ps[row] : a.s.top_p;
       const float min_p = a.s.min_ps ? a.s.min_ps[row] : a.s.min_p;
       const bool greedy = !(temperature > 0.0f), by_k = top_k > 0 && top_k < a.vocab, by_p = top_p < 1.0f;
+      s.own = -1;
       const uint64_t *box = s.hear();
       uint32_t besides[kPer];
       float tops[kPer], m = -INFINITY;
@@ -1023,20 +1154,20 @@ __global__ __launch_bounds__(W * 32 + 32, W == 8 ? 2 : 1) void sample_kernel(con
 constexpr int kDevices = 16;   // whose occupancy is kept
 
 template <int W>
-constexpr int kMostSteps = (int)(((227 << 10) - sizeof(Picks<W>) - 1024) / (2 * 32 * 16));
+constexpr int kMostSteps = (int)(((226 << 10) - sizeof(Picks<W>)) / (2 * 32 * 16));
 
 template <typename T, int W>
 int run_sample(SampleArgs a, int size, int log2, cudaStream_t stream) {
   static std::atomic<int> fits[kDevices][4][kMostSteps<W> + 1];   // clusters at once, by size and steps (0: not known)
   auto kernel = sample_kernel<T, W>;
   constexpr int kThreads = W * 32 + 32;
-  const size_t shared = (size_t)a.steps * 2 * 32 * 16;
+  const size_t shared = (size_t)a.steps * 2 * 32 * 16 + sizeof(Picks<W>);
   int device = 0, most = 0;
   cudaError_t e = cudaGetDevice(&device);
   if (e != cudaSuccess) return note_cuda(e);
   if (device < kDevices) most = fits[device][log2][a.steps].load(std::memory_order_relaxed);
   if (most == 0) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSteps<W> * 2 * 32 * 16);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSteps<W> * 2 * 32 * 16 + (int)sizeof(Picks<W>));
     if (e == cudaSuccess) e = launch_rows(kernel, a, 1, size, kThreads, shared, stream, &most);
     if (e != cudaSuccess) return note_cuda(e);
     if (most < 1) return SEQSUM_ECUDA;
