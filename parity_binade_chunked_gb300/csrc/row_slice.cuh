@@ -424,12 +424,12 @@ struct Stream {
   }
   __device__ __forceinline__ int32_t index(int32_t vec, int e) const { return (begin + vec) * kE + e - off; }
 
-  // the producer warp: brings `row` in; `full` counts two arrivals
-  __device__ __forceinline__ void bring(const T *row, uint64_t *full) const {
-    const int lane = threadIdx.x & 31;
-    const bool head = off > 0 && begin == 0 && n > 0, tail = n > 0 && index(n, 0) > vocab;
-    const int32_t from = head ? 1 : 0, to = n - (tail ? 1 : 0);
-    if (lane == 0) {
+  __device__ __forceinline__ bool cut_head() const { return off > 0 && begin == 0 && n > 0; }
+  __device__ __forceinline__ bool cut_tail() const { return n > 0 && index(n, 0) > vocab; }
+  // One warp brings `row` in; `full` counts two arrivals.  First what lies inside ...
+  __device__ __forceinline__ void bring_inner(const T *row, uint64_t *full) const {
+    if ((threadIdx.x & 31) == 0) {
+      const int32_t from = cut_head() ? 1 : 0, to = n - (cut_tail() ? 1 : 0);
       // (what was written to the buffer element by element, some rows ago, comes before the copy)
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       const uint32_t bytes = to > from ? (uint32_t)(to - from) * 16 : 0;
@@ -440,18 +440,30 @@ struct Stream {
                      "l"(row + index(from, 0)), "r"(bytes), "r"(smem(full))
                      : "memory");
     }
+  }
+  // ... then the elements of the vectors that stick out: lane e has element e
+  // of the first vector, lane 16 + e that of the last ...
+  __device__ __forceinline__ float edge(const T *row) const {
+    const int lane = threadIdx.x & 31, e = lane & 15;
+    if (e < kE && (lane < 16 ? cut_head() : cut_tail())) {
+      const int32_t i = index(lane < 16 ? 0 : n - 1, e);
+      if (i >= 0 && i < vocab) return Elem<T>::load(row + i);
+    }
+    return -INFINITY;
+  }
+  // ... which go into the buffer, with -inf up to the end of the last step.
+  __device__ __forceinline__ void bring_edges(float v, uint64_t *full) const {
+    const int lane = threadIdx.x & 31, e = lane & 15;
     constexpr uint32_t ninf = Elem<T>::kNegInf;
     if (lane >= (n & 31) && (n & 31)) buf[(n & ~31) + lane] = make_uint4(ninf, ninf, ninf, ninf);
-    if (head || tail) {
-      const int e = lane & 15;
-      const int32_t vec = lane < 16 ? 0 : n - 1;
-      if (e < kE && (lane < 16 ? head : tail)) {
-        const int32_t i = index(vec, e);
-        Elem<T>::store(reinterpret_cast<T *>(buf + vec) + e, i >= 0 && i < vocab ? Elem<T>::load(row + i) : -INFINITY);
-      }
-    }
+    if (e < kE && (lane < 16 ? cut_head() : cut_tail()))
+      Elem<T>::store(reinterpret_cast<T *>(buf + (lane < 16 ? 0 : n - 1)) + e, v);
     __syncwarp();
     if (lane == 0) bar_arrive(full);
+  }
+  __device__ __forceinline__ void bring(const T *row, uint64_t *full) const {
+    bring_inner(row, full);
+    bring_edges(edge(row), full);
   }
   // whether step `st` of the slice lies inside the row, all of it
   __device__ __forceinline__ bool inside(int32_t st) const {

@@ -363,7 +363,7 @@ struct Picks {
   uint64_t full[2], empty[2], told[4], gate[2];
   uint64_t box[4][kBoxes];        // a word of every warp of the cluster
   uint64_t step_mass[32];         // of the segment that the token is in
-  uint64_t mass[W], above[W];     // of the warps' entries; of those before the listed ones
+  uint64_t mass[W], above[2][W];  // of the warps' entries; of those before a split
   uint32_t heads[kBins];          // entries by eighths of an octave
   uint4 bins[2][kBins];           // a split: count, and mass in two halves
   uint32_t bin_count[kBins];      // ... summed over whom it concerns
@@ -511,16 +511,12 @@ struct Picker {
       }
     }
   }
-  // ... or, once there is one, of the list
+  // ... or of the list
   template <typename F>
-  __device__ __forceinline__ void entries(F f) const {
-    if (listed < 0) {
-      row_entries(kFloor, f);
-    } else {
-      for (int32_t i = threadIdx.x; i < listed; i += kThreads) {
-        const uint2 v = sh.all[i];
-        f(-__uint_as_float(v.x), (int32_t)v.y);
-      }
+  __device__ __forceinline__ void list_entries(F f) const {
+    for (int32_t i = threadIdx.x; i < listed; i += kThreads) {
+      const uint2 v = sh.all[i];
+      f(-__uint_as_float(v.x), (int32_t)v.y);
     }
   }
 
@@ -532,32 +528,73 @@ struct Picker {
     atomicAdd(&bins[bin].y, w & 0xffffu);   // a CTA has less than 2^16 entries: the halves' sums fit 32 bits
     atomicAdd(&bins[bin].z, w >> 16);
   }
-  // Entries by bin_of(key, index), where that is below kBins, and the first
-  // bin at which their count (or mass) reaches `need`.  With `from` above
-  // kFloor (over the row, by mass) only entries from there on are looked at,
-  // and those that bin_of puts into kBefore come before all bins.
-  static constexpr uint32_t kBefore = ~0u;
-  template <typename B>
-  __device__ Found find(bool by_mass, uint64_t need, B bin_of, float from = kFloor) {
-    uint4 *bins = sh.bins[gated & 1];   // (in turn: others of the cluster may still read the last one)
+  // Entries that a search goes on in: keys [lo, hi), or, where that is one
+  // key, indices [ilo, ihi) of it.  A first split (scale > 0) is even in
+  // octaves: by a power of two, from an eighth of an octave, so that
+  // differences and products are exact and each bin is a range of keys.
+  struct Range {
+    uint32_t lo, hi;
+    int32_t ilo, ihi;
+    float from, scale;
+    __device__ __forceinline__ void eighths(int e0, int e1, int32_t vocab) {
+      from = e0 * 0.125f;
+      lo = __float_as_uint(from), hi = __float_as_uint(e1 * 0.125f);
+      ilo = 0, ihi = vocab;
+      scale = 8.0f;
+      for (int n = e1 - e0; n <= kBins / 2; n *= 2) scale *= 2.0f;
+    }
+    __device__ __forceinline__ bool ties() const { return hi - lo == 1; }
+    __device__ __forceinline__ bool holds(uint32_t key, int32_t i) const {
+      return key >= lo && key < hi && (!ties() || (i >= ilo && i < ihi));
+    }
+    __device__ __forceinline__ int shift() const {
+      const uint32_t width = ties() ? (uint32_t)(ihi - ilo) : hi - lo;
+      return max(0, 32 - __clz(width - 1) - 8);
+    }
+    __device__ __forceinline__ void take_bin(int bin) {
+      if (scale > 0.0f) {
+        const float f = from;
+        lo = __float_as_uint(f + bin / scale), hi = __float_as_uint(f + (bin + 1) / scale);
+        scale = 0.0f;
+      } else if (const int s = shift(); ties()) {
+        ilo += bin << s;
+        ihi = min(ihi, ilo + (1 << s));
+      } else {
+        lo += (uint32_t)bin << s;
+        hi = min(hi, lo + (1u << s));
+      }
+    }
+  };
+
+  // Splits the entries of `r` and finds the first bin at which their count (or
+  // mass) reaches `need`.  Over the row, entries from `from` octaves on are
+  // looked at, and the mass of those before `r` comes before all bins.
+  __device__ Found find(bool by_mass, uint64_t need, const Range &r, float from) {
+    // (tables in turn: others of the cluster may still read the last ones)
+    uint4 *bins = sh.bins[gated & 1];
+    uint64_t *above = sh.above[gated & 1];
     if (threadIdx.x < kBins) bins[threadIdx.x] = make_uint4(0, 0, 0, 0);
     team();
     uint64_t front = 0;
+    const int shift = r.scale > 0.0f ? 0 : r.shift();
     auto take = [&](float d, int32_t i) {
-      const uint32_t b = bin_of(key_of(d), i);
-      if (b < (uint32_t)kBins) put(bins, b, d);
-      else if (b == kBefore) front += weight(d);
+      const uint32_t key = key_of(d);
+      if (r.holds(key, i))
+        put(bins, r.scale > 0.0f ? (uint32_t)((-d - r.from) * r.scale) : (r.ties() ? (uint32_t)(i - r.ilo) : key - r.lo) >> shift, d);
+      else if (r.scale > 0.0f && key < r.lo)
+        front += weight(d);
     };
-    if (from > kFloor) {
+    if (listed < 0) {
       row_entries(from, take);
       front = warp_sum(front);
-      if ((threadIdx.x & 31) == 0) sh.above[threadIdx.x >> 5] = front;
+      if ((threadIdx.x & 31) == 0) above[threadIdx.x >> 5] = front;
+      gather();
+      front = r.scale > 0.0f ? of_all(above) : 0;
     } else {
-      entries(take);
+      list_entries(take);
+      team();
+      front = 0;
     }
-    if (listed < 0) gather();
-    else team();
-    front = from > kFloor ? of_all(sh.above) : 0;
     if (threadIdx.x < kBins) {
       uint32_t n = 0;
       uint64_t w = 0;
@@ -587,7 +624,7 @@ struct Picker {
     uint32_t nb = __reduce_add_sync(~0u, lane < o ? n : 0);
     uint64_t wb = front + warp_sum(lane < o ? w : 0);
     Found f = {-1, 0, 0, 0, wb};
-    if (front >= need) return team(), f;   // reached before all bins
+    if (by_mass && front >= need) return team(), f;   // reached before all bins
     if (o < 32) {
       // (every lane goes through that lane's bins)
       f.bin = o * kPer;
@@ -602,77 +639,15 @@ struct Picker {
     return f;
   }
 
-  // The end of the shortest prefix of the entries' order that has `need`
-  // entries (or `need` of mass), and its mass; without one the end of all.
-  // The entries' eighths of octaves lie in [eighth0, eighth1).
-  __device__ Place prefix(bool by_mass, uint64_t need, int eighth0, int eighth1, uint64_t *mass) {
-    float scale;
-    const float from = eighth0 * 0.125f;
-    const Found f = find(by_mass, need, even_split(eighth0, eighth1, scale));
-    if (f.bin < 0) {
-      *mass = f.mass_before;
-      return Place{0x7fffffffu, 0};
-    }
-    return narrow(by_mass, need, f, __float_as_uint(from + f.bin / scale), __float_as_uint(from + (f.bin + 1) / scale), mass);
-  }
-
-  // The first split is even in octaves: by a power of two, from an eighth, so
-  // that differences and products are exact and each bin is a range of keys.
-  __device__ __forceinline__ static auto even_split(int eighth0, int eighth1, float &scale) {
-    scale = 8.0f;
-    for (int n = eighth1 - eighth0; n <= kBins / 2; n *= 2) scale *= 2.0f;
-    const float from = eighth0 * 0.125f, by = scale;
-    const uint32_t lo = __float_as_uint(from), hi = __float_as_uint(eighth1 * 0.125f);
-    return [=](uint32_t key, int32_t) {
-      return key < lo ? kBefore : key < hi ? (uint32_t)((__uint_as_float(key) - from) * by) : (uint32_t)kBins;
-    };
-  }
-
-  // ... from the bin `f` of keys [lo, hi) on.
-  __device__ Place narrow(bool by_mass, uint64_t need, Found f, uint32_t lo, uint32_t hi, uint64_t *mass) {
-    int32_t ilo = 0, ihi = x.vocab;
-    uint64_t before = 0;
-    while (ok) {
-      need -= by_mass ? f.mass_before : (uint64_t)f.count_before;
-      before += f.mass_before;
-      const bool ties = hi - lo == 1;
-      if (f.count == 1 || (by_mass ? need == f.mass : need == f.count)) {
-        *mass = before + f.mass;
-        return ties ? Place{lo, ihi} : Place{hi, 0};
-      }
-      auto inside = [&](uint32_t key, int32_t i) { return ties ? key == lo && i >= ilo && i < ihi : key >= lo && key < hi; };
-      if (listed < 0 && f.count <= (uint32_t)kList) {   // few enough now
-        list(__uint_as_float(lo), __uint_as_float(hi), inside);
-        if (!ok) break;
-      }
-      if (listed >= 0 && f.count <= 32) return last_few(by_mass, need, before, f.count, inside, mass);
-      // split keys [lo, hi), or, where that is one key, its indices [ilo, ihi)
-      const uint32_t width = ties ? (uint32_t)(ihi - ilo) : hi - lo;
-      const int shift = max(0, 32 - __clz(width - 1) - 8);
-      f = find(by_mass, need, [&](uint32_t key, int32_t i) {
-        return inside(key, i) ? (ties ? (uint32_t)(i - ilo) : key - lo) >> shift : (uint32_t)kBins;
-      });
-      if (f.bin < 0) break;   // (cannot be: the bin reached the need)
-      if (ties) {
-        ilo += f.bin << shift;
-        ihi = min(ihi, ilo + (1 << shift));
-      } else {
-        lo += (uint32_t)f.bin << shift;
-        hi = min(hi, lo + (1u << shift));
-      }
-    }
-    *mass = before;
-    return Place{hi, 0};
-  }
-
-  // At most 32 listed entries, `n` of them: each lane one, placed by counting.
-  template <typename I>
-  __device__ Place last_few(bool by_mass, uint64_t need, uint64_t before, uint32_t n, I inside, uint64_t *mass) {
+  // Of at most 32 listed entries in `r`, `n` of them, the one at which the
+  // count (or mass) reaches `need`: each lane has one, placed by counting.
+  // Its mass and that before it are added to *mass.
+  __device__ Place last_few(bool by_mass, uint64_t need, uint32_t n, const Range &r, uint64_t *mass) {
     if (threadIdx.x == 0) sh.small_listed = 0;
     team();
-    entries([&](float d, int32_t i) {
+    list_entries([&](float d, int32_t i) {
       const uint32_t key = key_of(d);
-      if (inside(key, i)) {
+      if (r.holds(key, i)) {
         const uint32_t at = atomicAdd(&sh.small_listed, 1u);
         if (at < 32) sh.small[at] = make_uint4(key, (uint32_t)i, weight(d), 0);
       }
@@ -681,202 +656,156 @@ struct Picker {
     const uint32_t lane = threadIdx.x & 31;
     const bool have = lane < n;
     const uint4 v = have ? sh.small[lane] : make_uint4(~0u, ~0u, 0, 0);
-    const uint32_t w = v.z;
     uint32_t count = 0;
     uint64_t sum = 0;
-#pragma unroll 8
+#pragma unroll 4
     for (uint32_t j = 0; j < n; j++) {
       const uint4 o = sh.small[j];
       if (o.x < v.x || (o.x == v.x && o.y < v.y)) count++, sum += o.z;
     }
-    const bool last = have && (by_mass ? sum < need && need <= sum + w : count + 1 == need);
+    const bool last = have && (by_mass ? sum < need && need <= sum + v.z : count + 1 == need);
     const int o = max(0, __ffs(__ballot_sync(~0u, last)) - 1);
-    *mass = before + __shfl_sync(~0u, sum + w, o);
+    *mass += __shfl_sync(~0u, sum + v.z, o);
     const Place p = {__shfl_sync(~0u, v.x, o), (int32_t)__shfl_sync(~0u, v.y, o) + 1};
     team();
     return p;
   }
 
-  // ---- lists
-
-  // Lists the row's entries at -d in [t0, t1) that are `inside`, every CTA all
-  // of them; returns the mass of those at -d below t0.  More than kList of
+  // Lists the row's entries in `r`, every CTA all of them.  More than kList of
   // them: `listed` stays -1.
-  template <typename I>
-  __device__ uint64_t list(float t0, float t1, I inside, bool want_above = false) {
+  __device__ void list(const Range &r) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (lists++ > 0) gather();   // nobody still reads this row's list before
     if (threadIdx.x == 0) sh.listed = 0;
     team();
-    uint64_t above = 0;
-    row_entries(fmaxf(kFloor, -t1), [&](float d, int32_t i) {
+    row_entries(fmaxf(kFloor, -__uint_as_float(r.hi)), [&](float d, int32_t i) {
       const uint32_t key = key_of(d);
-      if (-d < t0) {
-        if (want_above) above += weight(d);
-      } else if (-d < t1 && inside(key, i)) {
+      if (r.holds(key, i)) {
         const uint32_t at = atomicAdd(&sh.listed, 1u);
         if (at < (uint32_t)kList) sh.list[at] = make_uint2(key, (uint32_t)i);
       }
     });
-    if (want_above) {
-      above = warp_sum(above);
-      if (lane == 0) sh.above[warp] = above;
-    }
     gather();
     const uint32_t theirs = lane < (int)size ? ld_remote32(remote(&sh.listed, lane)) : 0;
-    const uint64_t before = want_above ? of_all(sh.above) : 0;
     const uint32_t ends = warp_scan(theirs, lane), total = __shfl_sync(~0u, ends, 31);
     if (total <= (uint32_t)kList) {
       listed = (int32_t)total;
-      for (uint32_t r = warp; r < size; r += W) {
-        const uint32_t have = __shfl_sync(~0u, theirs, r), at = __shfl_sync(~0u, ends, r) - have;
+      for (uint32_t c = warp; c < size; c += W) {
+        const uint32_t have = __shfl_sync(~0u, theirs, c), at = __shfl_sync(~0u, ends, c) - have;
         for (uint32_t i = lane; i < have; i += 32) {
-          const uint64_t v = ld_remote64(remote(&sh.list[i], r));
+          const uint64_t v = ld_remote64(remote(&sh.list[i], c));
           sh.all[at + i] = make_uint2((uint32_t)v, (uint32_t)(v >> 32));
         }
       }
     }
     team();
-    return before;
   }
 
-  // ---- the kept prefix
-
-  // Where the prefix that top-k and top-p keep ends.  `least` is a lower bound
-  // of the k-th largest entry's octaves.
-  __device__ Place kept_prefix(int32_t top_k, bool by_p, float top_p, float least) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    constexpr int kPer = kBins / 32;
-    bool by_k = top_k > 0 && top_k < x.vocab;
-    auto any = [](uint32_t, int32_t) { return true; };
-    uint64_t mass = 0;
-    listed = -1;
-    lists = 0;
-    if (by_k && least > kFloor) {
-      // not many more than k entries as a rule: all of them at once
-      const int eighth1 = min(kBins, (int)(-least * 8.0f) + 1);
-      list(0.0f, eighth1 * 0.125f, any);
-      if (listed >= 0 || !ok) {
-        Place end = prefix(false, top_k, 0, eighth1, &mass);
-        if (by_p) end = prefix(true, max((uint64_t)1, share(part_of(top_p), mass)), 0, eighth1, &mass);
-        return end;
-      }
-    }
-    if (threadIdx.x < kBins) sh.heads[threadIdx.x] = 0;
-    team();
-    if (!by_k) {
-      // The mass of all, exactly, and every kE-th entry's eighth: the mass of
-      // the tail by eighths, nearly, and so the eighths that the cut is in.
-      // That they hold it shows when their entries are summed; if they do not,
-      // the counts below are exact.
-      uint64_t mine = 0;
-#pragma unroll 2
-      for (int32_t st = st0; st < st1; st++) {
-        float d[kE];
-        octaves(x.buf[st * 32 + lane], d);
-        uint64_t of_vec = 0;
-#pragma unroll
-        for (int e = 0; e < kE; e += 2) of_vec += (uint64_t)weight(d[e]) + weight(d[e + 1]);
-        mine += of_vec;
-        if (d[0] > kFloor) atomicAdd(&sh.heads[(int)(-d[0] * 8.0f)], 1u);
-      }
-      mine = warp_sum(mine);
-      if (lane == 0) sh.mass[warp] = mine;
-      gather();
-      if (threadIdx.x < kBins) {
-        uint32_t n = 0;
-        for (uint32_t r = 0; r < size; r++) n += ld_remote32(remote(&sh.heads[threadIdx.x], r));
-        sh.bin_count[threadIdx.x] = n;
-      }
-      const uint64_t all = max((uint64_t)1, of_all(sh.mass));
-      const uint64_t cut = max((uint64_t)1, share(part_of(top_p), all));
-      team();
-      // the tail from each eighth on: its mass and that of its squares, from the back
-      auto middle = [&](int i) { return ex2(30.9375f - (lane * kPer + i) * 0.125f); };
-      float w[kPer], tail = 0.0f, tail2 = 0.0f;
-#pragma unroll
-      for (int i = 0; i < kPer; i++) {
-        w[i] = (float)sh.bin_count[lane * kPer + i] * (middle(i) * kE);
-        tail += w[i], tail2 += w[i] * (middle(i) * kE);
-      }
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const float u = __shfl_down_sync(~0u, tail, o), u2 = __shfl_down_sync(~0u, tail2, o);
-        if (lane + o < 32) tail += u, tail2 += u2;
-      }
-      tail = __shfl_down_sync(~0u, tail, 1), tail2 = __shfl_down_sync(~0u, tail2, 1);   // after the lane's bins
-      if (lane == 31) tail = tail2 = 0.0f;
-      const float left = (float)(all - cut);   // of mass, after the cut
-      int b0 = 0, b1 = kBins;
-#pragma unroll
-      for (int i = kPer - 1; i >= 0; i--) {
-        tail += w[i], tail2 += w[i] * (middle(i) * kE);
-        const float off = 0.05f * tail + 4.0f * sqrtf(tail2);
-        if (tail - off > left) b0 = max(b0, lane * kPer + i);
-        if (tail + off <= left) b1 = lane * kPer + i;
-      }
-      const int eighth0 = (int)__reduce_max_sync(~0u, (uint32_t)b0);
-      const int eighth1 = max((int)__reduce_min_sync(~0u, (uint32_t)b1), eighth0 + 1);
-      float scale;
-      const float from = eighth0 * 0.125f;
-      const auto bins = even_split(eighth0, eighth1, scale);
-      const float least1 = fmaxf(-eighth1 * 0.125f, kFloor + 1e-5f);
-      collect(least1);
-      const Found f = find(true, cut, bins, least1);
-      if (f.bin >= 0 || !ok)
-        return narrow(true, cut, f, __float_as_uint(from + f.bin / scale), __float_as_uint(from + (f.bin + 1) / scale), &mass);
-      if (threadIdx.x < kBins) sh.heads[threadIdx.x] = 0;   // (all have read them: they have met since)
-      team();
-    }
-    // counts by eighths of octaves, and the mass of all that may be kept
-    uint64_t mine = 0;
-    row_entries(least, [&](float d, int32_t) {
-      atomicAdd(&sh.heads[(int)(-d * 8.0f)], 1u);
-      if (by_p) mine += weight(d);
-    });
-    mine = warp_sum(mine);
-    if (lane == 0) sh.mass[warp] = mine;
-    gather();
+  // The cluster's sums of sh.heads, in sh.bin_count.
+  __device__ void sum_heads() {
     if (threadIdx.x < kBins) {
       uint32_t n = 0;
       for (uint32_t r = 0; r < size; r++) n += ld_remote32(remote(&sh.heads[threadIdx.x], r));
       sh.bin_count[threadIdx.x] = n;
     }
-    const uint64_t all = max((uint64_t)1, of_all(sh.mass));
     team();
+  }
+
+  // The mass of all, and by a sample (the first entry of each vector) the
+  // eighths of octaves [e0, e1) that the cut of top-p is in: where the tail's
+  // mass, give or take four standard deviations and a twentieth, can be what
+  // is left after the cut.  That they hold the cut shows when they are summed.
+  __device__ uint64_t sample(float top_p, int &e0, int &e1) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int kPer = kBins / 32;
+    uint64_t mine = 0;
+#pragma unroll 2
+    for (int32_t st = st0; st < st1; st++) {
+      float d[kE];
+      octaves(x.buf[st * 32 + lane], d);
+      uint64_t of_vec = 0;
+#pragma unroll
+      for (int e = 0; e < kE; e += 2) of_vec += (uint64_t)weight(d[e]) + weight(d[e + 1]);
+      mine += of_vec;
+      if (d[0] > kFloor) atomicAdd(&sh.heads[(int)(-d[0] * 8.0f)], 1u);
+    }
+    mine = warp_sum(mine);
+    if (lane == 0) sh.mass[warp] = mine;
+    gather();
+    const uint64_t all = max((uint64_t)1, of_all(sh.mass)), cut = max((uint64_t)1, share(part_of(top_p), all));
+    sum_heads();
+    auto middle = [&](int i) { return ex2(30.9375f - (lane * kPer + i) * 0.125f) * kE; };
+    float w[kPer], tail = 0.0f, tail2 = 0.0f;   // the tail's mass from an eighth on, and its variance
+#pragma unroll
+    for (int i = 0; i < kPer; i++) {
+      w[i] = (float)sh.bin_count[lane * kPer + i] * middle(i);
+      tail += w[i], tail2 += w[i] * middle(i);
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const float u = __shfl_down_sync(~0u, tail, o), u2 = __shfl_down_sync(~0u, tail2, o);
+      if (lane + o < 32) tail += u, tail2 += u2;
+    }
+    tail = __shfl_down_sync(~0u, tail, 1), tail2 = __shfl_down_sync(~0u, tail2, 1);   // after the lane's bins
+    if (lane == 31) tail = tail2 = 0.0f;
+    const float left = (float)(all - cut);
+    int b0 = 0, b1 = kBins;
+#pragma unroll
+    for (int i = kPer - 1; i >= 0; i--) {
+      tail += w[i], tail2 += w[i] * middle(i);
+      const float off = 0.05f * tail + 4.0f * sqrtf(tail2);
+      if (tail - off > left) b0 = max(b0, lane * kPer + i);
+      if (tail + off <= left) b1 = lane * kPer + i;
+    }
+    e0 = (int)__reduce_max_sync(~0u, (uint32_t)b0);
+    e1 = max((int)__reduce_min_sync(~0u, (uint32_t)b1), e0 + 1);
+    return cut;
+  }
+
+  // Counts by eighths, exactly, of the entries from `least` octaves on; the
+  // eighth in which the k-th is (0 where there are fewer, e1 is 0 then), or
+  // those that the cut of top-p can be in: bounds of the mass before each from
+  // the counts, from the front and, narrower in the tail, from the back.
+  __device__ uint64_t count(int32_t top_k, float least, float top_p, int &e0, int &e1) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int kPer = kBins / 32;
+    uint64_t mine = 0;
+    row_entries(least, [&](float d, int32_t) {
+      atomicAdd(&sh.heads[(int)(-d * 8.0f)], 1u);
+      mine += weight(d);
+    });
+    mine = warp_sum(mine);
+    if (lane == 0) sh.mass[warp] = mine;
+    gather();
+    const uint64_t all = max((uint64_t)1, of_all(sh.mass)), cut = max((uint64_t)1, share(part_of(top_p), all));
+    sum_heads();
     uint32_t counts[kPer], n = 0;
 #pragma unroll
     for (int i = 0; i < kPer; i++) n += counts[i] = sh.bin_count[lane * kPer + i];
-    const uint32_t upto = warp_scan(n, lane), total = __shfl_sync(~0u, upto, 31);
-    if (by_k && total < (uint32_t)top_k) by_k = false;   // all that weighs anything is among the first k
-    if (!by_k && !by_p) return Place{0x7fffffffu, 0};
-
-    if (by_k) {
-      // the eighth in which the count reaches k
-      const int o = __ffs(__ballot_sync(~0u, upto >= (uint32_t)top_k)) - 1;
-      uint32_t before = __shfl_sync(~0u, upto - n, o);
-      int b = o * kPer;
-      while (before + sh.bin_count[b] < (uint32_t)top_k) before += sh.bin_count[b++];
-      const uint64_t above = list(b * 0.125f, (b + 1) * 0.125f, any, true);
-      Place end = prefix(false, (uint32_t)top_k - before, b, b + 1, &mass);
-      if (by_p) {
-        listed = -1;
-        end = prefix(true, max((uint64_t)1, share(part_of(top_p), above + mass)), 0, b + 1, &mass);
+    const uint32_t upto = warp_scan(n, lane);
+    if (top_k > 0) {
+      const uint32_t reached = __ballot_sync(~0u, upto >= (uint32_t)top_k);
+      e0 = e1 = 0;
+      if (reached) {
+        const int o = __ffs(reached) - 1;
+        uint32_t before = __shfl_sync(~0u, upto - n, o);
+        e0 = o * kPer;
+        while (before + sh.bin_count[e0] < (uint32_t)top_k) before += sh.bin_count[e0++];
+        e1 = e0 + 1;
+        return (uint32_t)top_k - before;
       }
-      return end;
+      return 0;
     }
-    // The eighths that the cut can be in: bounds of the mass before each, from
-    // the counts, from the front and, narrower in the tail, from the back.
-    const uint64_t cut = max((uint64_t)1, share(part_of(top_p), all));
-    uint64_t lo[kPer], hi[kPer], least_mass = 0, most_mass = 0;
+    uint64_t lo[kPer], hi[kPer], least_before = 0, most_before = 0;
 #pragma unroll
     for (int i = 0; i < kPer; i++) {
       const float top = ex2(31.0f - (lane * kPer + i) * 0.125f);   // 2^(-1/8) = 0.9170040...
       lo[i] = counts[i] * (uint64_t)fmaxf(top * (0.9170040f * 0.99999f) - 2.0f, 0.0f);
       hi[i] = counts[i] * ((uint64_t)(top * 1.00001f) + 2);
-      least_mass += lo[i], most_mass += hi[i];
+      least_before += lo[i], most_before += hi[i];
     }
-    uint64_t least_before = warp_scan(least_mass, lane), most_before = warp_scan(most_mass, lane);
+    const uint64_t least_mass = least_before, most_mass = most_before;
+    least_before = warp_scan(least_before, lane), most_before = warp_scan(most_before, lane);
     const uint64_t least_all = __shfl_sync(~0u, least_before, 31), most_all = __shfl_sync(~0u, most_before, 31);
     least_before -= least_mass, most_before -= most_mass;
     int b0 = 0, b1 = kBins;
@@ -888,17 +817,103 @@ struct Picker {
       if (at_least >= cut) b1 = min(b1, lane * kPer + i);
       least_before += lo[i], most_before += hi[i];
     }
-    const int eighth0 = (int)__reduce_max_sync(~0u, (uint32_t)b0);
-    const int eighth1 = max((int)__reduce_min_sync(~0u, (uint32_t)b1), eighth0 + 1);
-    const float t1 = eighth1 * 0.125f;
-    const uint64_t above = list(eighth0 * 0.125f, t1, any, true);
-    const Place end = prefix(true, cut - above, eighth0, eighth1, &mass);
-    return end.key == 0x7fffffffu ? Place{__float_as_uint(t1), 0} : end;
+    e0 = (int)__reduce_max_sync(~0u, (uint32_t)b0);
+    e1 = max((int)__reduce_min_sync(~0u, (uint32_t)b1), e0 + 1);
+    return cut;
+  }
+
+  // ---- the kept prefix
+
+  // Where the prefix that top-k and top-p keep ends.  `least` is a lower bound
+  // of the k-th largest entry's octaves.  Up to two searches, first for the
+  // k-th entry, then for the cut of top-p: the shortest prefix of the order
+  // that has k entries, or the cut's mass.
+  __device__ Place kept_prefix(int32_t top_k, bool by_p, float top_p, float least) {
+    bool by_k = top_k > 0 && top_k < x.vocab;
+    enum { kAll, kSample, kCount, kGo } how = by_k && least > kFloor ? kAll : by_k ? kCount : kSample;
+    listed = -1;
+    lists = 0;
+    Range r;
+    int e0 = 0, e1 = kBins;
+    uint64_t need = top_k, mass = 0, bin_mass = 0;
+    uint32_t bin_count = ~0u;
+    float from = kFloor;
+    bool sampled = false, all_listed = false;
+    while (ok) {
+      if (how != kGo) {
+        // a search begins
+        if (how == kAll) {   // not many more than k entries as a rule: all of them at once
+          e0 = 0, e1 = min(kBins, (int)(-least * 8.0f) + 1);
+        } else {
+          if (threadIdx.x < kBins) sh.heads[threadIdx.x] = 0;   // (last read before others of the cluster were met again)
+          team();
+          if (how == kSample) {
+            need = sample(top_p, e0, e1);
+          } else {
+            need = count(by_k ? top_k : 0, least, top_p, e0, e1);
+            if (by_k && e1 == 0) {   // all that weighs anything is among the first k
+              if (!by_p) break;
+              by_k = false;
+              how = kSample;
+              gather();
+              continue;
+            }
+          }
+          from = fmaxf(-e1 * 0.125f, kFloor + 1e-5f);
+          if (how == kCount && e1 == kBins) from = kFloor;
+          sampled = how == kSample;
+          if (!by_k) collect(from);
+        }
+        r.eighths(e0, e1, x.vocab);
+        mass = 0, bin_count = ~0u;
+      }
+      if (listed < 0 && (how == kAll || bin_count <= (uint32_t)kList)) {   // few enough
+        list(r);
+        if (!ok) break;
+        all_listed = how == kAll && listed >= 0;
+        if (how == kAll && listed < 0) {
+          how = kCount;
+          gather();
+          continue;
+        }
+      }
+      how = kGo;
+      Place end;
+      if (bin_count <= 32 && listed >= 0 && r.scale == 0.0f) {
+        end = last_few(by_k ? false : true, need, bin_count, r, &mass);
+      } else if (r.scale == 0.0f && (bin_count == 1 || need == (by_k ? (uint64_t)bin_count : bin_mass))) {
+        mass += bin_mass;
+        end = r.ties() ? Place{r.lo, r.ihi} : Place{r.hi, 0};
+      } else {
+        const Found f = find(!by_k, need, r, from);
+        if (f.bin < 0) {
+          if (!sampled) return Place{r.hi, 0};   // (cannot be: what is not reached is less than all)
+          how = kCount;                          // the sample misled
+          gather();
+          continue;
+        }
+        need -= by_k ? (uint64_t)f.count_before : f.mass_before;
+        mass += f.mass_before;
+        bin_count = f.count, bin_mass = f.mass;
+        r.take_bin(f.bin);
+        continue;
+      }
+      if (!by_k || !by_p) return end;
+      // the second search, among those up to here
+      by_k = false;
+      need = max((uint64_t)1, share(part_of(top_p), mass));
+      const int last = min(kBins, (int)(__uint_as_float(end.key) * 8.0f) + 1);
+      if (!all_listed) listed = -1;
+      r.eighths(0, last, x.vocab);
+      from = fmaxf(-last * 0.125f, kFloor);
+      mass = 0, bin_count = ~0u;
+    }
+    return Place{0x7fffffffu, 0};
   }
 };
 
 template <typename T, int W>
-__global__ __launch_bounds__(W * 32 + 32, W == 8 ? 2 : 1) void sample_kernel(const SampleArgs a) {
+__global__ __launch_bounds__(W * 32, W == 8 ? 2 : 1) void sample_kernel(const SampleArgs a) {
   extern __shared__ uint4 buffers[];   // two buffers of a.steps steps, and the rest
   Picks<W> &sh = *reinterpret_cast<Picks<W> *>(buffers + 2 * a.steps * 32);
   constexpr int kE = Elem<T>::kPerVec, kLog2W = W == 16 ? 4 : 3;
@@ -927,14 +942,11 @@ __global__ __launch_bounds__(W * 32 + 32, W == 8 ? 2 : 1) void sample_kernel(con
     x.set(static_cast<const T *>(a.logits) + row_of(it) * a.stride, a.vocab, rank, log2_size, buffers + (it & 1) * a.steps * 32);
     return x;
   };
-  if (warp == W) {
-    bool ok = true;
-    for (uint32_t it = 0; it < turns; it++) {
-      if (it > 1) ok = __all_sync(~0u, bar_wait(&sh.empty[it & 1], ((it >> 1) - 1) & 1));
-      if (!ok) break;
-      stream(it).bring(static_cast<const T *>(a.logits) + row_of(it) * a.stride, &sh.full[it & 1]);
-    }
-  } else {
+  // The first warp brings rows in, the copy first, later in the same turn what
+  // sticks out of it.  (A warp for that alone would leave the others 96
+  // registers and 250 bytes of spills, which shared memory this large sends to L2.)
+  auto row_at = [&](uint32_t it) { return static_cast<const T *>(a.logits) + row_of(it) * a.stride; };
+  {
     Picker<T, W> s(sh);
     s.rank = rank, s.size = size;
     constexpr int kPer = (kMaxCluster * W + 31) / 32;
@@ -986,9 +998,27 @@ __global__ __launch_bounds__(W * 32 + 32, W == 8 ? 2 : 1) void sample_kernel(con
       s.post(((uint64_t)beside << 32) | __float_as_uint(m));
     };
 
+    if (warp == 0)
+      for (uint32_t i = 0; i < 2 && i < turns; i++) {
+        const Stream<T> x = stream(i);
+        x.bring_inner(row_at(i), &sh.full[i]);
+        x.bring_edges(x.edge(row_at(i)), &sh.full[i]);
+      }
     look(0);
     uint32_t it = 0;
     for (; it < turns; it++) {
+      // the row after next goes where the last one was
+      float edge = 0.0f;
+      bool bring = warp == 0 && it > 0 && it + 1 < turns;
+      if (bring) {
+        s.came &= bar_wait(&sh.empty[(it - 1) & 1], ((it - 1) >> 1) & 1);
+        bring = __all_sync(~0u, s.came);   // (if not, the CTA's next agreement ends it)
+      }
+      if (bring) {
+        const Stream<T> x = stream(it + 1);
+        x.bring_inner(row_at(it + 1), &sh.full[(it + 1) & 1]);
+        edge = x.edge(row_at(it + 1));
+      }
       // the second part: what is kept of the row, and its mass by warps
       const int64_t row = row_of(it);
       if (it > 0) place(it);
@@ -1067,6 +1097,7 @@ __global__ __launch_bounds__(W * 32 + 32, W == 8 ? 2 : 1) void sample_kernel(con
         s.post(warp_sum(mine));
       }
 
+      if (bring) stream(it + 1).bring_edges(edge, &sh.full[(it + 1) & 1]);
       // the next row's first part, while the words of this one travel
       if (it + 1 < turns) look(it + 1);
 
@@ -1160,7 +1191,7 @@ template <typename T, int W>
 int run_sample(SampleArgs a, int size, int log2, cudaStream_t stream) {
   static std::atomic<int> fits[kDevices][4][kMostSteps<W> + 1];   // clusters at once, by size and steps (0: not known)
   auto kernel = sample_kernel<T, W>;
-  constexpr int kThreads = W * 32 + 32;
+  constexpr int kThreads = W * 32;
   const size_t shared = (size_t)a.steps * 2 * 32 * 16 + sizeof(Picks<W>);
   int device = 0, most = 0;
   cudaError_t e = cudaGetDevice(&device);
