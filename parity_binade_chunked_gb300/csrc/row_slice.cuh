@@ -143,17 +143,12 @@ __device__ __forceinline__ void st_remote(uint32_t a, uint64_t v) {
 }
 __device__ __forceinline__ uint64_t ld_remote64(uint32_t a) {
   uint64_t v;
-  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint4 ld_remote128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a));
   return v;
 }
 __device__ __forceinline__ uint32_t ld_remote32(uint32_t a) {
   uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
 }
 
@@ -373,14 +368,18 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity) {
   return bar_try(bar, parity) || bar_wait_long(bar, parity);
 }
 
-// One arrival of the calling warp at `bar` of every CTA: what its lanes wrote
-// to shared memory before is seen by who waits for it.  A barrier of the
-// cluster's working warps needs two such in turn.
-__device__ __forceinline__ void arrive_everywhere(uint64_t *bar, uint32_t size) {
-  const uint32_t lane = threadIdx.x & 31;
-  __syncwarp();
-  if (lane < size)
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote(bar, lane)) : "memory");
+// 16 bytes to shared memory of CTA `rank`, counted down at its `bar`.
+__device__ __forceinline__ void send(uint4 *to, uint64_t *bar, uint32_t rank, uint4 v) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+                   remote(to, rank)),
+               "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"(remote(bar, rank))
+               : "memory");
+}
+__device__ __forceinline__ void send(uint2 *to, uint64_t *bar, uint32_t rank, uint2 v) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(
+                   remote(to, rank)),
+               "r"(v.x), "r"(v.y), "r"(remote(bar, rank))
+               : "memory");
 }
 
 struct Exchange {

@@ -360,14 +360,12 @@ constexpr int kOwn = 192;     // ... that a warp can of its segment
 template <int W>
 struct Picks {
   static constexpr int kBoxes = kMaxCluster * W;
-  uint64_t full[2], empty[2], told[4], gate[2];
+  uint64_t full[2], empty[2], told[4], parts, totals, entries;
   uint64_t box[4][kBoxes];        // a word of every warp of the cluster
   uint64_t step_mass[32];         // of the segment that the token is in
-  uint64_t mass[W], above[2][W];  // of the warps' entries; of those before a split
-  uint32_t heads[kBins];          // entries by eighths of an octave
-  uint4 bins[2][kBins];           // a split: count, and mass in two halves
-  uint32_t bin_count[kBins];      // ... summed over whom it concerns
-  uint64_t bin_mass[kBins];
+  uint4 bins[kBins];              // a split of the CTA's entries: count, and mass in two halves
+  uint4 part[kBins];              // this CTA's share of the bins, of every CTA
+  uint4 total[kBins];             // the bins summed over the cluster: count, mass
   uint32_t listed, small_listed;
   uint4 small[32];                // the last few entries of a search: key, index, weight
   uint2 list[kList], all[kList];  // (key, index): this CTA's entries, the row's
@@ -385,13 +383,12 @@ struct Picker {
   static constexpr int kE = Elem<T>::kPerVec, kThreads = W * 32;
   Picks<W> &sh;
   Stream<T> x;
-  uint32_t rank, size, posted = 0, heard = 0, gated = 0;
+  uint32_t rank, size, posted = 0, heard = 0, totalled = 0, shared_lists = 0;
   int32_t st0, st1;     // this warp's steps
   float m, c;
   bool special;         // (v - m) * c needs care
   bool came = true;     // no wait of this warp gave up
   bool ok = true;       // ... none of the CTA's, as of the last agreement
-  int lists = 0;        // made for this row
   int own = -1;         // entries that this warp took out of its segment, from own_from octaves on
   float own_from = 0.0f;
   int32_t listed = -1;  // entries of sh.all, once a search goes over those; -1: over the row
@@ -426,21 +423,58 @@ struct Picker {
     if (threadIdx.x == 0) bar_expect(&sh.told[b], size * W * 8);
     return sh.box[b];
   }
-  // what any working thread of the cluster wrote to shared memory before is seen after
-  __device__ __forceinline__ void gather() {
-    uint64_t *bar = &sh.gate[gated & 1];
-    const uint32_t parity = (gated >> 1) & 1;
-    gated++;
-    arrive_everywhere(bar, size);
-    came &= bar_wait(bar, parity);
+  // The sum of the words heard.
+  __device__ __forceinline__ uint64_t sum_of(const uint64_t *box) const {
+    constexpr int kPer = (kMaxCluster * W + 31) / 32;
+    uint64_t sum = 0;
+#pragma unroll
+    for (int k = 0; k < kPer; k++) {
+      const uint32_t i = (threadIdx.x & 31) + 32 * k;
+      if (i < size * W) sum += box[i];
+    }
+    return warp_sum(sum);
+  }
+  // sh.bins of every CTA, once all its warps are through, summed into sh.total
+  // of each: every CTA sums its share of the bins and sends the sums around.
+  // (Sent with asynchronous stores: a release of plain ones to the cluster
+  // took 1300 to 5000 cycles, reading 256 bins of 8 CTAs 2000.)
+  __device__ __forceinline__ void total_bins() {
+    team();
+    if (size == 1) {
+      if (threadIdx.x < kBins) {
+        const uint4 v = sh.bins[threadIdx.x];
+        const uint64_t w = v.y + ((uint64_t)v.z << 16);
+        sh.total[threadIdx.x] = make_uint4(v.x, (uint32_t)w, (uint32_t)(w >> 32), 0);
+      }
+      team();
+      return;
+    }
+    const uint32_t share = kBins / size, to = threadIdx.x / share, bin = threadIdx.x % share, parity = totalled++ & 1;
+    if (threadIdx.x < kBins) {
+      const uint4 v = sh.bins[threadIdx.x];
+      const uint64_t w = v.y + ((uint64_t)v.z << 16);
+      send(&sh.part[rank * share + bin], &sh.parts, to, make_uint4(v.x, (uint32_t)w, (uint32_t)(w >> 32), 0));
+    }
+    came &= bar_wait(&sh.parts, parity);
+    if (threadIdx.x == 0) bar_expect(&sh.parts, kBins * 16);
+    if (threadIdx.x < kBins) {
+      uint32_t n = 0;
+      uint64_t w = 0;
+#pragma unroll
+      for (uint32_t c = 0; c < kMaxCluster; c++)
+        if (c < size) {
+          const uint4 v = sh.part[c * share + bin];
+          n += v.x, w += v.y + ((uint64_t)v.z << 32);
+        }
+      send(&sh.total[rank * share + bin], &sh.totals, to, make_uint4(n, (uint32_t)w, (uint32_t)(w >> 32), 0));
+    }
+    came &= bar_wait(&sh.totals, parity);
+    if (threadIdx.x == 0) bar_expect(&sh.totals, kBins * 16);
     agree();
   }
-
-  // The sum of all warps' words in a shared table of each CTA.
-  __device__ __forceinline__ uint64_t of_all(const uint64_t *table) const {
-    uint64_t v = 0;
-    for (uint32_t i = threadIdx.x & 31; i < size * W; i += 32) v += ld_remote64(remote(&table[i % W], i / W));
-    return warp_sum(v);
+  __device__ __forceinline__ void clear_bins() {
+    if (threadIdx.x < kBins) sh.bins[threadIdx.x] = make_uint4(0, 0, 0, 0);
+    team();
   }
 
   // ---- entries
@@ -570,70 +604,66 @@ struct Picker {
   // mass) reaches `need`.  Over the row, entries from `from` octaves on are
   // looked at, and the mass of those before `r` comes before all bins.
   __device__ Found find(bool by_mass, uint64_t need, const Range &r, float from) {
-    // (tables in turn: others of the cluster may still read the last ones)
-    uint4 *bins = sh.bins[gated & 1];
-    uint64_t *above = sh.above[gated & 1];
-    if (threadIdx.x < kBins) bins[threadIdx.x] = make_uint4(0, 0, 0, 0);
-    team();
+    clear_bins();
     uint64_t front = 0;
     const int shift = r.scale > 0.0f ? 0 : r.shift();
     auto take = [&](float d, int32_t i) {
       const uint32_t key = key_of(d);
       if (r.holds(key, i))
-        put(bins, r.scale > 0.0f ? (uint32_t)((-d - r.from) * r.scale) : (r.ties() ? (uint32_t)(i - r.ilo) : key - r.lo) >> shift, d);
+        put(sh.bins, r.scale > 0.0f ? (uint32_t)((-d - r.from) * r.scale) : (r.ties() ? (uint32_t)(i - r.ilo) : key - r.lo) >> shift, d);
       else if (r.scale > 0.0f && key < r.lo)
         front += weight(d);
     };
     if (listed < 0) {
       row_entries(from, take);
-      front = warp_sum(front);
-      if ((threadIdx.x & 31) == 0) above[threadIdx.x >> 5] = front;
-      gather();
-      front = r.scale > 0.0f ? of_all(above) : 0;
+      if (r.scale > 0.0f) post(warp_sum(front));
+      total_bins();
+      front = r.scale > 0.0f ? sum_of(hear()) : 0;
     } else {
       list_entries(take);
       team();
+      if (threadIdx.x < kBins) {
+        const uint4 v = sh.bins[threadIdx.x];
+        const uint64_t w = v.y + ((uint64_t)v.z << 16);
+        sh.total[threadIdx.x] = make_uint4(v.x, (uint32_t)w, (uint32_t)(w >> 32), 0);
+      }
+      team();
       front = 0;
     }
-    if (threadIdx.x < kBins) {
-      uint32_t n = 0;
-      uint64_t w = 0;
-      if (listed < 0) {
-        for (uint32_t r = 0; r < size; r++) {
-          const uint4 v = ld_remote128(remote(&bins[threadIdx.x], r));
-          n += v.x, w += v.y + ((uint64_t)v.z << 16);
-        }
-      } else {
-        const uint4 v = bins[threadIdx.x];
-        n = v.x, w = v.y + ((uint64_t)v.z << 16);
-      }
-      sh.bin_count[threadIdx.x] = n;
-      sh.bin_mass[threadIdx.x] = w;
-    }
-    team();
-    // every warp for itself: lane l has bins 8 l to 8 l + 7
+    // Every warp for itself: lane l has bins 8 l to 8 l + 7; then, of the lane
+    // whose bins reach it, each of the first eight lanes a bin.
     constexpr int kPer = kBins / 32;
     const int lane = threadIdx.x & 31;
     uint32_t n = 0;
     uint64_t w = 0;
 #pragma unroll
-    for (int i = 0; i < kPer; i++) n += sh.bin_count[lane * kPer + i], w += sh.bin_mass[lane * kPer + i];
+    for (int i = 0; i < kPer; i++) {
+      const uint4 v = sh.total[lane * kPer + i];
+      n += v.x, w += v.y + ((uint64_t)v.z << 32);
+    }
     const uint64_t upto = by_mass ? front + warp_scan(w, lane) : warp_scan(n, lane);
     const uint32_t reached = __ballot_sync(~0u, need <= upto);
-    const int o = reached ? __ffs(reached) - 1 : 32;   // the lane whose bins reach it
-    uint32_t nb = __reduce_add_sync(~0u, lane < o ? n : 0);
-    uint64_t wb = front + warp_sum(lane < o ? w : 0);
-    Found f = {-1, 0, 0, 0, wb};
-    if (by_mass && front >= need) return team(), f;   // reached before all bins
-    if (o < 32) {
-      // (every lane goes through that lane's bins)
-      f.bin = o * kPer;
-      for (;; f.bin++) {
-        f.count = sh.bin_count[f.bin], f.mass = sh.bin_mass[f.bin];
-        if ((by_mass ? wb + f.mass : (uint64_t)nb + f.count) >= need) break;
-        nb += f.count, wb += f.mass;
+    Found f = {-1, 0, 0, 0, 0};
+    if (reached && !(by_mass && front >= need)) {
+      const int o = __ffs(reached) - 1;
+      const uint32_t nb = __reduce_add_sync(~0u, lane < o ? n : 0);
+      const uint64_t wb = front + warp_sum(lane < o ? w : 0);
+      const uint4 v = sh.total[o * kPer + lane % kPer];
+      uint32_t n8 = v.x;
+      uint64_t w8 = v.y + ((uint64_t)v.z << 32);
+#pragma unroll
+      for (int d = 1; d < kPer; d <<= 1) {
+        const uint32_t nu = __shfl_up_sync(~0u, n8, d);
+        const uint64_t wu = __shfl_up_sync(~0u, w8, d);
+        if (lane % kPer >= d) n8 += nu, w8 += wu;
       }
-      f.count_before = nb, f.mass_before = wb;
+      const int at = __ffs(__ballot_sync(~0u, by_mass ? need <= wb + w8 : need <= (uint64_t)nb + n8)) - 1;
+      f.bin = o * kPer + at;
+      const uint32_t n_at = __shfl_sync(~0u, v.x, at);
+      const uint64_t w_at = __shfl_sync(~0u, v.y + ((uint64_t)v.z << 32), at);
+      f.count = n_at, f.mass = w_at;
+      f.count_before = nb + __shfl_sync(~0u, n8, at) - n_at;
+      f.mass_before = wb + __shfl_sync(~0u, w8, at) - w_at;
     }
     team();   // the sums may be written again
     return f;
@@ -675,7 +705,6 @@ struct Picker {
   // them: `listed` stays -1.
   __device__ void list(const Range &r) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (lists++ > 0) gather();   // nobody still reads this row's list before
     if (threadIdx.x == 0) sh.listed = 0;
     team();
     row_entries(fmaxf(kFloor, -__uint_as_float(r.hi)), [&](float d, int32_t i) {
@@ -685,30 +714,29 @@ struct Picker {
         if (at < (uint32_t)kList) sh.list[at] = make_uint2(key, (uint32_t)i);
       }
     });
-    gather();
-    const uint32_t theirs = lane < (int)size ? ld_remote32(remote(&sh.listed, lane)) : 0;
-    const uint32_t ends = warp_scan(theirs, lane), total = __shfl_sync(~0u, ends, 31);
-    if (total <= (uint32_t)kList) {
-      listed = (int32_t)total;
-      for (uint32_t c = warp; c < size; c += W) {
-        const uint32_t have = __shfl_sync(~0u, theirs, c), at = __shfl_sync(~0u, ends, c) - have;
-        for (uint32_t i = lane; i < have; i += 32) {
-          const uint64_t v = ld_remote64(remote(&sh.list[i], c));
-          sh.all[at + i] = make_uint2((uint32_t)v, (uint32_t)(v >> 32));
-        }
+    team();
+    const uint32_t mine = sh.listed;
+    if (size == 1) {
+      if (mine <= (uint32_t)kList) {
+        for (uint32_t i = threadIdx.x; i < mine; i += kThreads) sh.all[i] = sh.list[i];
+        listed = (int32_t)mine;
       }
+      team();
+      return;
     }
-    team();
-  }
-
-  // The cluster's sums of sh.heads, in sh.bin_count.
-  __device__ void sum_heads() {
-    if (threadIdx.x < kBins) {
-      uint32_t n = 0;
-      for (uint32_t r = 0; r < size; r++) n += ld_remote32(remote(&sh.heads[threadIdx.x], r));
-      sh.bin_count[threadIdx.x] = n;
-    }
-    team();
+    post(warp == 0 ? mine : 0);
+    const uint64_t *box = hear();
+    const uint32_t theirs = lane < (int)size ? (uint32_t)box[lane * W] : 0;
+    const uint32_t ends = warp_scan(theirs, lane), total = __shfl_sync(~0u, ends, 31);
+    agree();
+    if (total > (uint32_t)kList || !ok) return;
+    // each entry goes to every CTA, whose barrier counts them all
+    const uint32_t at = __shfl_sync(~0u, ends - theirs, rank);
+    for (uint32_t i = threadIdx.x; i < mine * size; i += kThreads) send(&sh.all[at + i / size], &sh.entries, i % size, sh.list[i / size]);
+    if (threadIdx.x == 0) bar_expect(&sh.entries, total * 8);
+    came &= bar_wait(&sh.entries, shared_lists++ & 1);
+    agree();
+    listed = (int32_t)total;
   }
 
   // The mass of all, and by a sample (the first entry of each vector) the
@@ -716,8 +744,9 @@ struct Picker {
   // mass, give or take four standard deviations and a twentieth, can be what
   // is left after the cut.  That they hold the cut shows when they are summed.
   __device__ uint64_t sample(float top_p, int &e0, int &e1) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
     constexpr int kPer = kBins / 32;
+    clear_bins();
     uint64_t mine = 0;
 #pragma unroll 2
     for (int32_t st = st0; st < st1; st++) {
@@ -727,18 +756,16 @@ struct Picker {
 #pragma unroll
       for (int e = 0; e < kE; e += 2) of_vec += (uint64_t)weight(d[e]) + weight(d[e + 1]);
       mine += of_vec;
-      if (d[0] > kFloor) atomicAdd(&sh.heads[(int)(-d[0] * 8.0f)], 1u);
+      if (d[0] > kFloor) atomicAdd(&sh.bins[(int)(-d[0] * 8.0f)].x, 1u);
     }
-    mine = warp_sum(mine);
-    if (lane == 0) sh.mass[warp] = mine;
-    gather();
-    const uint64_t all = max((uint64_t)1, of_all(sh.mass)), cut = max((uint64_t)1, share(part_of(top_p), all));
-    sum_heads();
+    post(warp_sum(mine));
+    total_bins();
+    const uint64_t all = max((uint64_t)1, sum_of(hear())), cut = max((uint64_t)1, share(part_of(top_p), all));
     auto middle = [&](int i) { return ex2(30.9375f - (lane * kPer + i) * 0.125f) * kE; };
     float w[kPer], tail = 0.0f, tail2 = 0.0f;   // the tail's mass from an eighth on, and its variance
 #pragma unroll
     for (int i = 0; i < kPer; i++) {
-      w[i] = (float)sh.bin_count[lane * kPer + i] * middle(i);
+      w[i] = (float)sh.total[lane * kPer + i].x * middle(i);
       tail += w[i], tail2 += w[i] * middle(i);
     }
 #pragma unroll
@@ -753,7 +780,9 @@ struct Picker {
 #pragma unroll
     for (int i = kPer - 1; i >= 0; i--) {
       tail += w[i], tail2 += w[i] * middle(i);
-      const float off = 0.05f * tail + 4.0f * sqrtf(tail2);
+      float root;
+      asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(root) : "f"(tail2));
+      const float off = 0.05f * tail + 4.0f * root;
       if (tail - off > left) b0 = max(b0, lane * kPer + i);
       if (tail + off <= left) b1 = lane * kPer + i;
     }
@@ -767,21 +796,20 @@ struct Picker {
   // those that the cut of top-p can be in: bounds of the mass before each from
   // the counts, from the front and, narrower in the tail, from the back.
   __device__ uint64_t count(int32_t top_k, float least, float top_p, int &e0, int &e1) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
     constexpr int kPer = kBins / 32;
+    clear_bins();
     uint64_t mine = 0;
     row_entries(least, [&](float d, int32_t) {
-      atomicAdd(&sh.heads[(int)(-d * 8.0f)], 1u);
+      atomicAdd(&sh.bins[(int)(-d * 8.0f)].x, 1u);
       mine += weight(d);
     });
-    mine = warp_sum(mine);
-    if (lane == 0) sh.mass[warp] = mine;
-    gather();
-    const uint64_t all = max((uint64_t)1, of_all(sh.mass)), cut = max((uint64_t)1, share(part_of(top_p), all));
-    sum_heads();
+    post(warp_sum(mine));
+    total_bins();
+    const uint64_t all = max((uint64_t)1, sum_of(hear())), cut = max((uint64_t)1, share(part_of(top_p), all));
     uint32_t counts[kPer], n = 0;
 #pragma unroll
-    for (int i = 0; i < kPer; i++) n += counts[i] = sh.bin_count[lane * kPer + i];
+    for (int i = 0; i < kPer; i++) n += counts[i] = sh.total[lane * kPer + i].x;
     const uint32_t upto = warp_scan(n, lane);
     if (top_k > 0) {
       const uint32_t reached = __ballot_sync(~0u, upto >= (uint32_t)top_k);
@@ -790,7 +818,7 @@ struct Picker {
         const int o = __ffs(reached) - 1;
         uint32_t before = __shfl_sync(~0u, upto - n, o);
         e0 = o * kPer;
-        while (before + sh.bin_count[e0] < (uint32_t)top_k) before += sh.bin_count[e0++];
+        while (before + sh.total[e0].x < (uint32_t)top_k) before += sh.total[e0++].x;
         e1 = e0 + 1;
         return (uint32_t)top_k - before;
       }
@@ -832,7 +860,6 @@ struct Picker {
     bool by_k = top_k > 0 && top_k < x.vocab;
     enum { kAll, kSample, kCount, kGo } how = by_k && least > kFloor ? kAll : by_k ? kCount : kSample;
     listed = -1;
-    lists = 0;
     Range r;
     int e0 = 0, e1 = kBins;
     uint64_t need = top_k, mass = 0, bin_mass = 0;
@@ -845,8 +872,6 @@ struct Picker {
         if (how == kAll) {   // not many more than k entries as a rule: all of them at once
           e0 = 0, e1 = min(kBins, (int)(-least * 8.0f) + 1);
         } else {
-          if (threadIdx.x < kBins) sh.heads[threadIdx.x] = 0;   // (last read before others of the cluster were met again)
-          team();
           if (how == kSample) {
             need = sample(top_p, e0, e1);
           } else {
@@ -855,7 +880,6 @@ struct Picker {
               if (!by_p) break;
               by_k = false;
               how = kSample;
-              gather();
               continue;
             }
           }
@@ -873,7 +897,6 @@ struct Picker {
         all_listed = how == kAll && listed >= 0;
         if (how == kAll && listed < 0) {
           how = kCount;
-          gather();
           continue;
         }
       }
@@ -889,7 +912,6 @@ struct Picker {
         if (f.bin < 0) {
           if (!sampled) return Place{r.hi, 0};   // (cannot be: what is not reached is less than all)
           how = kCount;                          // the sample misled
-          gather();
           continue;
         }
         need -= by_k ? (uint64_t)f.count_before : f.mass_before;
@@ -926,12 +948,14 @@ __global__ __launch_bounds__(W * 32, W == 8 ? 2 : 1) void sample_kernel(const Sa
     for (int b = 0; b < 2; b++) {
       bar_init(&sh.full[b], 2);
       bar_init(&sh.empty[b], W);
-      bar_init(&sh.gate[b], size * W);
     }
     for (int b = 0; b < 4; b++) {
       bar_init(&sh.told[b], 1);
       bar_expect(&sh.told[b], size * W * 8);
     }
+    bar_init(&sh.parts, 1), bar_expect(&sh.parts, kBins * 16);
+    bar_init(&sh.totals, 1), bar_expect(&sh.totals, kBins * 16);
+    bar_init(&sh.entries, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   cluster_sync();   // every CTA's barriers are ready
