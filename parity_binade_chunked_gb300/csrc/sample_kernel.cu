@@ -357,20 +357,26 @@ __global__ __launch_bounds__(NT) void sample_reread_kernel(const SampleArgs a) {
 constexpr int kList = 1280;   // entries that a search can take out of the row
 constexpr int kOwn = 192;     // ... that a warp can of its segment
 
-template <int W>
+// What the CTA's warps share, and what others of the cluster write to.  Calls
+// without top-k and top-p have no use for lists; they get a third buffer.
+template <int W, bool kSearch>
 struct Picks {
+  static constexpr int kBinsHere = kSearch ? kBins : 1, kListHere = kSearch ? kList : 1, kOwnHere = kSearch ? kOwn : 1;
   static constexpr int kBoxes = kMaxCluster * W;
-  uint64_t full[2], empty[2], told[4], parts, totals, entries;
+  uint64_t full[3], empty[3], told[4], parts, totals, entries;
   uint64_t box[4][kBoxes];        // a word of every warp of the cluster
   uint64_t step_mass[32];         // of the segment that the token is in
-  uint4 bins[kBins];              // a split of the CTA's entries: count, and mass in two halves
-  uint4 part[kBins];              // this CTA's share of the bins, of every CTA
-  uint4 total[kBins];             // the bins summed over the cluster: count, mass
+  uint4 bins[kBinsHere];              // a split of the CTA's entries: count, and mass in two halves
+  uint4 part[kBinsHere];              // this CTA's share of the bins, of every CTA
+  uint4 total[kBinsHere];             // the bins summed over the cluster: count, mass
   uint32_t listed, small_listed;
   uint4 small[32];                // the last few entries of a search: key, index, weight
-  uint2 list[kList], all[kList];  // (key, index): this CTA's entries, the row's
-  uint2 own[W][kOwn];             // a warp's
+  uint2 list[kListHere], all[kListHere];  // (key, index): this CTA's entries, the row's
+  uint2 own[W][kOwnHere];             // a warp's
 };
+
+template <bool kSearch>
+constexpr int kBuffers = kSearch ? 2 : 3;
 
 struct Found {
   int bin;                        // -1: the need is not reached
@@ -378,10 +384,10 @@ struct Found {
   uint64_t mass, mass_before;
 };
 
-template <typename T, int W>
+template <typename T, int W, bool kSearch>
 struct Picker {
   static constexpr int kE = Elem<T>::kPerVec, kThreads = W * 32;
-  Picks<W> &sh;
+  Picks<W, kSearch> &sh;
   Stream<T> x;
   uint32_t rank, size, posted = 0, heard = 0, totalled = 0, shared_lists = 0;
   int32_t st0, st1;     // this warp's steps
@@ -393,7 +399,7 @@ struct Picker {
   float own_from = 0.0f;
   int32_t listed = -1;  // entries of sh.all, once a search goes over those; -1: over the row
 
-  __device__ Picker(Picks<W> &s) : sh(s) {}
+  __device__ Picker(Picks<W, kSearch> &s) : sh(s) {}
 
   // ---- the CTA's working warps, and the cluster's
 
@@ -520,30 +526,63 @@ struct Picker {
     own = n <= kOwn ? n : -1;
     own_from = from;
   }
-  // f(octaves, index) of the row's entries from `from` octaves (at least kFloor) on in this thread
+  // f(octaves, index) of the row's entries from `from` octaves (at least
+  // kFloor) up to `to` in this thread
   template <typename F>
-  __device__ __forceinline__ void row_entries(float from, F f) const {
+  __device__ __forceinline__ void row_entries(float from, float to, F f) const {
     const int lane = threadIdx.x & 31;
     if (own >= 0 && from >= own_from) {
       for (int i = lane; i < own; i += 32) {
         const uint2 v = sh.own[threadIdx.x >> 5][i];
         const float d = -__uint_as_float(v.x);
-        if (d >= from) f(d, (int32_t)v.y);
+        if (d >= from && d <= to) f(d, (int32_t)v.y);
       }
       return;
     }
     const float least = reached_from(from);
-#pragma unroll 4
+#pragma unroll 1
+    for (int32_t st = st0; st < st1; st++) {
+      const uint4 w = x.buf[st * 32 + lane];
+      if (Elem<T>::vec_max(w, -INFINITY) >= least) {
+        float d[kE];
+        octaves(w, d);
+        bool any = false;
+#pragma unroll
+        for (int e = 0; e < kE; e++) any |= d[e] >= from && d[e] <= to;
+        if (any) {
+#pragma unroll
+          for (int e = 0; e < kE; e++)
+            if (d[e] >= from && d[e] <= to && d[e] > kFloor) f(d[e], x.index(st * 32 + lane, e));
+        }
+      }
+    }
+  }
+  // The sum of g(octaves, index) over them, where g is 0 for NaN and -inf
+  // (without branches: for rows of which many entries count).
+  template <typename G>
+  __device__ __forceinline__ uint64_t row_sum(float from, G g) const {
+    const int lane = threadIdx.x & 31;
+    uint64_t sum = 0;
+    if (own >= 0 && from >= own_from) {
+      for (int i = lane; i < own; i += 32) {
+        const uint2 v = sh.own[threadIdx.x >> 5][i];
+        sum += g(-__uint_as_float(v.x), (int32_t)v.y);
+      }
+      return warp_sum(sum);
+    }
+    const float least = reached_from(from);
+#pragma unroll 1
     for (int32_t st = st0; st < st1; st++) {
       const uint4 w = x.buf[st * 32 + lane];
       if (Elem<T>::vec_max(w, -INFINITY) >= least) {
         float d[kE];
         octaves(w, d);
 #pragma unroll
-        for (int e = 0; e < kE; e++)
-          if (d[e] >= from && d[e] > kFloor) f(d[e], x.index(st * 32 + lane, e));
+        for (int e = 0; e < kE; e += 2)
+          sum += (uint64_t)g(d[e], x.index(st * 32 + lane, e)) + g(d[e + 1], x.index(st * 32 + lane, e + 1));
       }
     }
+    return warp_sum(sum);
   }
   // ... or of the list
   template <typename F>
@@ -611,12 +650,11 @@ struct Picker {
       const uint32_t key = key_of(d);
       if (r.holds(key, i))
         put(sh.bins, r.scale > 0.0f ? (uint32_t)((-d - r.from) * r.scale) : (r.ties() ? (uint32_t)(i - r.ilo) : key - r.lo) >> shift, d);
-      else if (r.scale > 0.0f && key < r.lo)
-        front += weight(d);
     };
     if (listed < 0) {
-      row_entries(from, take);
-      if (r.scale > 0.0f) post(warp_sum(front));
+      const float lo = __uint_as_float(r.lo);
+      if (r.scale > 0.0f) post(r.lo > 0 ? row_sum(from, [&](float d, int32_t) { return -d < lo ? weight(d) : 0; }) : 0);
+      row_entries(from, -lo, take);
       total_bins();
       front = r.scale > 0.0f ? sum_of(hear()) : 0;
     } else {
@@ -707,7 +745,7 @@ struct Picker {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) sh.listed = 0;
     team();
-    row_entries(fmaxf(kFloor, -__uint_as_float(r.hi)), [&](float d, int32_t i) {
+    row_entries(fmaxf(kFloor, -__uint_as_float(r.hi)), -__uint_as_float(r.lo), [&](float d, int32_t i) {
       const uint32_t key = key_of(d);
       if (r.holds(key, i)) {
         const uint32_t at = atomicAdd(&sh.listed, 1u);
@@ -748,7 +786,7 @@ struct Picker {
     constexpr int kPer = kBins / 32;
     clear_bins();
     uint64_t mine = 0;
-#pragma unroll 2
+#pragma unroll 1
     for (int32_t st = st0; st < st1; st++) {
       float d[kE];
       octaves(x.buf[st * 32 + lane], d);
@@ -800,7 +838,7 @@ struct Picker {
     constexpr int kPer = kBins / 32;
     clear_bins();
     uint64_t mine = 0;
-    row_entries(least, [&](float d, int32_t) {
+    row_entries(least, 0.0f, [&](float d, int32_t) {
       atomicAdd(&sh.bins[(int)(-d * 8.0f)].x, 1u);
       mine += weight(d);
     });
@@ -934,10 +972,11 @@ struct Picker {
   }
 };
 
-template <typename T, int W>
+template <typename T, int W, bool kSearch>
 __global__ __launch_bounds__(W * 32, W == 8 ? 2 : 1) void sample_kernel(const SampleArgs a) {
-  extern __shared__ uint4 buffers[];   // two buffers of a.steps steps, and the rest
-  Picks<W> &sh = *reinterpret_cast<Picks<W> *>(buffers + 2 * a.steps * 32);
+  constexpr int kB = kBuffers<kSearch>;
+  extern __shared__ uint4 buffers[];   // kB buffers of a.steps steps, and the rest
+  auto &sh = *reinterpret_cast<Picks<W, kSearch> *>(buffers + kB * a.steps * 32);
   constexpr int kE = Elem<T>::kPerVec, kLog2W = W == 16 ? 4 : 3;
   const uint32_t size = cluster_size(), rank = cluster_rank();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -945,7 +984,7 @@ __global__ __launch_bounds__(W * 32, W == 8 ? 2 : 1) void sample_kernel(const Sa
   const uint32_t turns = ((uint32_t)a.rows - first + step - 1) / step;   // (at most one cluster a row)
   const int log2_size = __ffs(size) - 1;
   if (threadIdx.x == 0) {
-    for (int b = 0; b < 2; b++) {
+    for (int b = 0; b < kB; b++) {
       bar_init(&sh.full[b], 2);
       bar_init(&sh.empty[b], W);
     }
@@ -963,7 +1002,7 @@ __global__ __launch_bounds__(W * 32, W == 8 ? 2 : 1) void sample_kernel(const Sa
   auto row_of = [&](uint32_t it) { return (int64_t)(first + it * step); };
   auto stream = [&](uint32_t it) {
     Stream<T> x;
-    x.set(static_cast<const T *>(a.logits) + row_of(it) * a.stride, a.vocab, rank, log2_size, buffers + (it & 1) * a.steps * 32);
+    x.set(static_cast<const T *>(a.logits) + row_of(it) * a.stride, a.vocab, rank, log2_size, buffers + it % kB * a.steps * 32);
     return x;
   };
   // The first warp brings rows in, the copy first, later in the same turn what
@@ -971,7 +1010,7 @@ __global__ __launch_bounds__(W * 32, W == 8 ? 2 : 1) void sample_kernel(const Sa
   // registers and 250 bytes of spills, which shared memory this large sends to L2.)
   auto row_at = [&](uint32_t it) { return static_cast<const T *>(a.logits) + row_of(it) * a.stride; };
   {
-    Picker<T, W> s(sh);
+    Picker<T, W, kSearch> s(sh);
     s.rank = rank, s.size = size;
     constexpr int kPer = (kMaxCluster * W + 31) / 32;
     const uint32_t half = size * W / 2;
@@ -991,7 +1030,7 @@ __global__ __launch_bounds__(W * 32, W == 8 ? 2 : 1) void sample_kernel(const Sa
       place(it);
       const bool greedy = !(temperature_of(row_of(it)) > 0.0f);
       const int32_t top_k = top_k_of(row_of(it));
-      s.came &= bar_wait(&sh.full[it & 1], (it >> 1) & 1);
+      s.came &= bar_wait(&sh.full[it % kB], it / kB & 1);
       float m = -INFINITY;
 #pragma unroll 4
       for (int32_t st = s.st0; st < s.st1; st++) m = Elem<T>::vec_max(s.x.buf[st * 32 + lane], m);
@@ -1008,7 +1047,7 @@ __global__ __launch_bounds__(W * 32, W == 8 ? 2 : 1) void sample_kernel(const Sa
             if (v[e] == m) beside = min(beside, (uint32_t)s.x.index(st * 32 + lane, e));
         }
         beside = __reduce_min_sync(~0u, beside);
-      } else if (top_k > 0 && top_k < a.vocab) {
+      } else if (kSearch && top_k > 0 && top_k < a.vocab) {
         const uint32_t j = ((uint32_t)top_k + half - 1) / half;
         if (j <= 32) {
           uint32_t mine = ordered(of_thread);
@@ -1023,7 +1062,7 @@ __global__ __launch_bounds__(W * 32, W == 8 ? 2 : 1) void sample_kernel(const Sa
     };
 
     if (warp == 0)
-      for (uint32_t i = 0; i < 2 && i < turns; i++) {
+      for (uint32_t i = 0; i < kB && i < turns; i++) {
         const Stream<T> x = stream(i);
         x.bring_inner(row_at(i), &sh.full[i]);
         x.bring_edges(x.edge(row_at(i)), &sh.full[i]);
@@ -1031,17 +1070,18 @@ __global__ __launch_bounds__(W * 32, W == 8 ? 2 : 1) void sample_kernel(const Sa
     look(0);
     uint32_t it = 0;
     for (; it < turns; it++) {
-      // the row after next goes where the last one was
+      // a row goes where the last one was
+      const uint32_t next = it + kB - 1;
       float edge = 0.0f;
-      bool bring = warp == 0 && it > 0 && it + 1 < turns;
+      bool bring = warp == 0 && it > 0 && next < turns;
       if (bring) {
-        s.came &= bar_wait(&sh.empty[(it - 1) & 1], ((it - 1) >> 1) & 1);
+        s.came &= bar_wait(&sh.empty[(it - 1) % kB], (it - 1) / kB & 1);
         bring = __all_sync(~0u, s.came);   // (if not, the CTA's next agreement ends it)
       }
       if (bring) {
-        const Stream<T> x = stream(it + 1);
-        x.bring_inner(row_at(it + 1), &sh.full[(it + 1) & 1]);
-        edge = x.edge(row_at(it + 1));
+        const Stream<T> x = stream(next);
+        x.bring_inner(row_at(next), &sh.full[next % kB]);
+        edge = x.edge(row_at(next));
       }
       // the second part: what is kept of the row, and its mass by warps
       const int64_t row = row_of(it);
@@ -1050,7 +1090,7 @@ __global__ __launch_bounds__(W * 32, W == 8 ? 2 : 1) void sample_kernel(const Sa
       const int32_t top_k = top_k_of(row);
       const float top_p = a.s.top_ps ? a.s.top_ps[row] : a.s.top_p;
       const float min_p = a.s.min_ps ? a.s.min_ps[row] : a.s.min_p;
-      const bool greedy = !(temperature > 0.0f), by_k = top_k > 0 && top_k < a.vocab, by_p = top_p < 1.0f;
+      const bool greedy = !(temperature > 0.0f), by_k = kSearch && top_k > 0 && top_k < a.vocab, by_p = kSearch && top_p < 1.0f;
       s.own = -1;
       const uint64_t *box = s.hear();
       uint32_t besides[kPer];
@@ -1070,10 +1110,8 @@ __global__ __launch_bounds__(W * 32, W == 8 ? 2 : 1) void sample_kernel(const Sa
       Place end = {0x7fffffffu, 0};
       const uint32_t floor_w = min_p > 0.0f ? __float2uint_rn(fminf(min_p, 1.0f) * 2147483648.0f) : 0;
       auto kept = [&](float d, int32_t i) -> uint32_t {
-        const uint32_t q = key_of(d);
-        if (!(q < end.key || (q == end.key && i < end.index))) return 0;
-        const uint32_t w = weight(d);
-        return w >= floor_w ? w : 0;
+        const uint32_t q = key_of(d), w = weight(d);   // (0 for NaN and -inf)
+        return w >= floor_w && (q < end.key || (q == end.key && i < end.index)) ? w : 0;
       };
       const bool draw = m > -INFINITY && !greedy;
       if (m == -INFINITY) {   // nothing left to choose from
@@ -1089,7 +1127,7 @@ __global__ __launch_bounds__(W * 32, W == 8 ? 2 : 1) void sample_kernel(const Sa
         s.m = m;
         s.c = __fdiv_rn(1.44269504f, temperature);
         s.special = !(m < INFINITY && s.c < INFINITY);
-        if (by_k || by_p) {
+        if constexpr (kSearch) if (by_k || by_p) {
           float least = kFloor;
           if (by_k) {
             // a number that one warp of each two reaches: half of them
@@ -1104,8 +1142,9 @@ __global__ __launch_bounds__(W * 32, W == 8 ? 2 : 1) void sample_kernel(const Sa
           end = s.kept_prefix(top_k, by_p, top_p, least);
           if (!s.ok) break;
         }
-        uint64_t mine = 0;
+        uint64_t mine;
         if (!by_k && !by_p && floor_w == 0) {
+          mine = 0;
 #pragma unroll 4
           for (int32_t st = s.st0; st < s.st1; st++) {
             float d[kE];
@@ -1115,13 +1154,14 @@ __global__ __launch_bounds__(W * 32, W == 8 ? 2 : 1) void sample_kernel(const Sa
             for (int e = 0; e < kE; e += 2) of_vec += (uint64_t)weight(d[e]) + weight(d[e + 1]);   // 0 from kFloor on, and for NaN
             mine += of_vec;
           }
+          mine = warp_sum(mine);
         } else {
-          s.row_entries(fmaxf(kFloor, -__uint_as_float(end.key)), [&](float d, int32_t i) { mine += kept(d, i); });
+          mine = s.row_sum(fmaxf(kFloor, -__uint_as_float(end.key)), kept);
         }
-        s.post(warp_sum(mine));
+        s.post(mine);
       }
 
-      if (bring) stream(it + 1).bring_edges(edge, &sh.full[(it + 1) & 1]);
+      if (bring) stream(next).bring_edges(edge, &sh.full[next % kB]);
       // the next row's first part, while the words of this one travel
       if (it + 1 < turns) look(it + 1);
 
@@ -1192,13 +1232,13 @@ __global__ __launch_bounds__(W * 32, W == 8 ? 2 : 1) void sample_kernel(const Sa
         if (!s.ok) break;
       }
       __syncwarp();
-      if (lane == 0) bar_arrive(&sh.empty[it & 1]);
+      if (lane == 0) bar_arrive(&sh.empty[it % kB]);
     }
     if (!s.ok) {
       // a wait gave up: what is not done is marked, copies in flight land before the CTA goes
       if (rank == 0 && threadIdx.x == 0)
         for (; it < turns; it++) a.tokens[row_of(it)] = -1, a.logps[row_of(it)] = NAN;
-      for (int b = 0; b < 2; b++)
+      for (int b = 0; b < kB; b++)
         for (uint32_t parity = 0; parity < 2; parity++) bar_wait(&sh.full[b], parity);
     }
   }
@@ -1208,21 +1248,22 @@ __global__ __launch_bounds__(W * 32, W == 8 ? 2 : 1) void sample_kernel(const Sa
 
 constexpr int kDevices = 16;   // whose occupancy is kept
 
-template <int W>
-constexpr int kMostSteps = (int)(((226 << 10) - sizeof(Picks<W>)) / (2 * 32 * 16));
+template <int W, bool kSearch>
+constexpr int kMostSteps = (int)(((226 << 10) - sizeof(Picks<W, kSearch>)) / (kBuffers<kSearch> * 32 * 16));
 
-template <typename T, int W>
+template <typename T, int W, bool kSearch>
 int run_sample(SampleArgs a, int size, int log2, cudaStream_t stream) {
-  static std::atomic<int> fits[kDevices][4][kMostSteps<W> + 1];   // clusters at once, by size and steps (0: not known)
-  auto kernel = sample_kernel<T, W>;
+  static std::atomic<int> fits[kDevices][4][kMostSteps<W, kSearch> + 1];   // clusters at once, by size and steps (0: not known)
+  auto kernel = sample_kernel<T, W, kSearch>;
   constexpr int kThreads = W * 32;
-  const size_t shared = (size_t)a.steps * 2 * 32 * 16 + sizeof(Picks<W>);
+  const size_t shared = (size_t)a.steps * kBuffers<kSearch> * 32 * 16 + sizeof(Picks<W, kSearch>);
   int device = 0, most = 0;
   cudaError_t e = cudaGetDevice(&device);
   if (e != cudaSuccess) return note_cuda(e);
   if (device < kDevices) most = fits[device][log2][a.steps].load(std::memory_order_relaxed);
   if (most == 0) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSteps<W> * 2 * 32 * 16 + (int)sizeof(Picks<W>));
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSteps<W, kSearch> * kBuffers<kSearch> * 32 * 16 +
+                             (int)sizeof(Picks<W, kSearch>));
     if (e == cudaSuccess) e = launch_rows(kernel, a, 1, size, kThreads, shared, stream, &most);
     if (e != cudaSuccess) return note_cuda(e);
     if (most < 1) return SEQSUM_ECUDA;
@@ -1243,12 +1284,15 @@ int choose_sample(SampleArgs a, cudaStream_t stream) {
   while (size < kMaxCluster && (steps > (int64_t)size * 66 || (a.rows * size * 2 <= sms && steps > (int64_t)size * 8)))
     size *= 2, log2++;
   a.steps = (int32_t)((steps + size - 1) / size);
-  if (a.steps > kMostSteps<16>) {
+  // (three buffers where there is room for them)
+  const bool search = a.s.top_ks || a.s.top_ps || a.s.top_k > 0 || a.s.top_p < 1.0f || a.steps > kMostSteps<16, false>;
+  if (a.steps > kMostSteps<16, true>) {
     const cudaError_t e = launch_rows(sample_reread_kernel<T, 512>, a, a.rows, kMaxCluster, 512, 0, stream);
     return e == cudaSuccess ? SEQSUM_OK : note_cuda(e);
   }
   // (one CTA an SM from 66 steps on: then twice the warps)
-  return a.steps > 66 ? run_sample<T, 16>(a, size, log2, stream) : run_sample<T, 8>(a, size, log2, stream);
+  if (search) return a.steps > 66 ? run_sample<T, 16, true>(a, size, log2, stream) : run_sample<T, 8, true>(a, size, log2, stream);
+  return a.steps > 66 ? run_sample<T, 16, false>(a, size, log2, stream) : run_sample<T, 8, false>(a, size, log2, stream);
 }
 
 }  // namespace
