@@ -15,7 +15,6 @@ import torch
 from . import SeqsumError, _check, lib
 
 _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
-_SETTINGS = (("temperature", torch.float32), ("top_k", torch.int32), ("top_p", torch.float32), ("min_p", torch.float32))
 
 
 class _Sampling(ctypes.Structure):
@@ -102,6 +101,12 @@ def _vector(t, name, n, dtype, index):
     return t.data_ptr()
 
 
+def _number(v, name):
+    if v != v:
+        raise ValueError(f"{name} is NaN")
+    return v
+
+
 def _output(t, name, n, dtype, index, like, stream):
     """A given output, checked, or a new one: the tensor and its address."""
     if t is None:
@@ -120,21 +125,28 @@ def sample_tokens(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tok
     in the order top-k, top-p, min-p.  The sums are integers: a row's token
     does not depend on the batch it is in."""
     rows, vocab, stride, dtype, index = _logits(logits)
-    one, each = [], []
-    for (name, kind), v in zip(_SETTINGS, (temperature, top_k, top_p, min_p)):
-        if isinstance(v, torch.Tensor):
-            each.append(_vector(v, name, rows, kind, index))
-            one.append(0)
-        elif v != v:
-            raise ValueError(f"{name} is NaN")
-        else:
-            each.append(None)
-            one.append(min(max(int(v), 0), 2 ** 31 - 1) if name == "top_k" else v)
+    s = _Sampling()
+    if isinstance(temperature, torch.Tensor):
+        s.temperatures = _vector(temperature, "temperature", rows, torch.float32, index)
+    else:
+        s.temperature = _number(temperature, "temperature")
+    if isinstance(top_k, torch.Tensor):
+        s.top_ks = _vector(top_k, "top_k", rows, torch.int32, index)
+    elif top_k > 0:
+        s.top_k = min(int(top_k), 2 ** 31 - 1)
+    if isinstance(top_p, torch.Tensor):
+        s.top_ps = _vector(top_p, "top_p", rows, torch.float32, index)
+    else:
+        s.top_p = _number(top_p, "top_p")
+    if isinstance(min_p, torch.Tensor):
+        s.min_ps = _vector(min_p, "min_p", rows, torch.float32, index)
+    else:
+        s.min_p = _number(min_p, "min_p")
     up = _vector(u, "u", rows, torch.float32, index)
     tokens, tp = _output(tokens, "tokens", rows, torch.int64, index, logits, stream)
     logps, lp = _output(logps, "logps", rows, torch.float32, index, logits, stream)
     _call(index, stream, _entries().seqsum_sample_tokens, logits.data_ptr(), dtype, rows, vocab, stride, up,
-          _Sampling(*one, *each), tp, lp)
+          s, tp, lp)
     return tokens, logps
 
 
