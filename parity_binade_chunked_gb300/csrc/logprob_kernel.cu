@@ -147,20 +147,26 @@ __device__ __forceinline__ bool same_alignment(const T *d, int32_t off) {
 
 constexpr int kBoxes = 4;   // exchanges under way, a power of two
 
-// Rows on chip in a CTA: one coming, one at work; and one more where a row's
-// gradient waits while the next row is summed.
-constexpr int kWarps = 8, kLog2Warps = 3;   // and the producer
+constexpr int kWarps = 8, kLog2Warps = 3;   // and one that brings rows in
+constexpr int kBuffers = 2;                 // one row coming, one at work
+// Whether the next row is summed before a row is finished, so that the words of
+// one travel while the other is worked on.  Not where a gradient is due: that
+// takes a third buffer, so one CTA an SM less (779 us for 8192 x 131072 bf16
+// rows instead of 695).
 template <bool kGrad>
-constexpr int kBuffers = 2;
-template <bool kGrad>
-constexpr int kLag = kGrad ? 0 : 1;   // whether the next row is summed before a row is finished
+constexpr int kLag = kGrad ? 0 : 1;
 
 // A cluster's rows one after another (see Stream): a row's segments, and the
-// sum and gradient of that row or the one before.
+// sum and gradient of that row or the one before.  An element is one subtraction
+// and one multiplication (two of each in an instruction), one ex2 and half an
+// addition; the gradient takes the exponentials again from the buffer rather
+// than room for them.  Bound by HBM with gradient: 8192 x 131072 bf16 695 us
+// (6.2 of 6.8 TB/s), 4000 x 50000 133 us (6.0).  Without: 4096 x 50001 70 us
+// (5.9 TB/s), 4096 x 131072 200 us (5.4), where issue slots are two thirds full.
 template <typename T, bool kGrad>
 __global__ __launch_bounds__(kWarps * 32 + 32) void logprob_kernel(const LogprobArgs a) {
   extern __shared__ uint4 buffers[];   // kB buffers of a.steps steps
-  constexpr int kE = Elem<T>::kPerVec, kB = kBuffers<kGrad>, kL = kLag<kGrad>;
+  constexpr int kE = Elem<T>::kPerVec, kB = kBuffers, kL = kLag<kGrad>;
   __shared__ uint64_t full[kB], empty[kB], told[kBoxes], box[kBoxes][kMaxCluster * kWarps];
   const uint32_t size = cluster_size(), rank = cluster_rank();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -208,7 +214,7 @@ __global__ __launch_bounds__(kWarps * 32 + 32) void logprob_kernel(const Logprob
         token = a.tokens[row_of(it)];
         if (kGrad) dlogp = a.dlogps[row_of(it)];
         ok &= bar_wait(&full[b], parity);
-        const Exchange tell = {box[it % kBoxes], &told[it % kBoxes], (uint32_t)segments * 8};
+        const Exchange tell = {box[it % kBoxes], &told[it % kBoxes]};
         int32_t st = x.step_of(segment, log2_segments) - x.begin / 32;
         const int32_t end = x.step_of(segment + 1, log2_segments) - x.begin / 32;
         Part part;
@@ -290,7 +296,7 @@ __global__ __launch_bounds__(kWarps * 32 + 32) void logprob_kernel(const Logprob
   cluster_sync();
 }
 
-// Short rows: a warp each, in registers.  (8192 x 3001 bf16 rows, gradient:
+// Short rows: a warp each, in registers; no barrier, no exchange.  (8192 x 3001 bf16 rows, gradient:
 // 29 us, the host's time; 46 us streamed.  4090: 49 and 51.)
 template <typename T, int KV, bool kGrad>
 __global__ __launch_bounds__(128) void logprob_short_kernel(const LogprobArgs a) {
@@ -337,8 +343,8 @@ __global__ __launch_bounds__(128) void logprob_short_kernel(const LogprobArgs a)
   }
 }
 
-// Rows too large for the buffers: one CTA a part of a row, its passes read
-// global memory (L2).
+// Rows too large for the buffers (beyond 8 x 112 KB): one CTA a part of a row,
+// its passes read global memory again (L2).
 template <typename T, int NT, bool kGrad>
 __global__ __launch_bounds__(NT) void logprob_reread_kernel(const LogprobArgs a) {
   __shared__ uint64_t box[kMaxCluster];
@@ -390,7 +396,9 @@ __global__ __launch_bounds__(NT) void logprob_reread_kernel(const LogprobArgs a)
   }
 }
 
-// With the row's lse given every element stands for itself.
+// With the row's lse given every element stands for itself: one read, one
+// write, 64 bytes a thread on the way.  Bound by HBM: 2048 x 32768 fp32 80 us
+// (6.7 of 6.8 TB/s).
 template <typename T, int KV, int NT>
 __global__ __launch_bounds__(NT) void backward_kernel(const LogprobArgs a) {
   const int64_t row = blockIdx.x / a.parts;
@@ -419,13 +427,8 @@ __global__ __launch_bounds__(NT) void backward_kernel(const LogprobArgs a) {
 constexpr int kDevices = 16;           // whose occupancy is kept
 constexpr int kShort = 12;             // steps of the rows that a warp takes by itself
 
-template <bool kGrad>
-constexpr size_t shared_bytes(int64_t steps) {
-  return (size_t)steps * kBuffers<kGrad> * 32 * 16;
-}
-// steps of a row that a CTA has room for
-template <bool kGrad>
-constexpr int kMostSteps = (224 << 10) / (kBuffers<kGrad> * 32 * 16);
+constexpr size_t shared_bytes(int64_t steps) { return (size_t)steps * kBuffers * 32 * 16; }
+constexpr int kMostSteps = (224 << 10) / (kBuffers * 32 * 16);   // of a row that a CTA has room for
 
 // CTAs a row, and how many such clusters run at once.  Two buffers of up to 52
 // KB let two CTAs share an SM (three up to 37 KB), so that some compute while
@@ -434,7 +437,7 @@ constexpr int kMostSteps = (224 << 10) / (kBuffers<kGrad> * 32 * 16);
 // 50000: 98 steps 133 us, 49 steps 155.)
 template <typename T, bool kGrad>
 int choose_logprob(LogprobArgs a, cudaStream_t stream) {
-  static std::atomic<int> fits[kDevices][4][kMostSteps<kGrad> + 1];   // clusters at once, by size and steps (0: not known)
+  static std::atomic<int> fits[kDevices][4][kMostSteps + 1];   // clusters at once, by size and steps (0: not known)
   constexpr int kE = Elem<T>::kPerVec;
   const int64_t vecs = ((int64_t)a.vocab + kE - 1) / kE + 1;   // whatever the alignment
   const int64_t steps = (vecs + 31) / 32;
@@ -449,18 +452,18 @@ int choose_logprob(LogprobArgs a, cudaStream_t stream) {
   while (size < kMaxCluster && steps > (int64_t)size * 104) size *= 2, log2++;
   a.steps = (int32_t)((steps + size - 1) / size);
   cudaError_t e;
-  if (a.steps > kMostSteps<kGrad>) {
+  if (a.steps > kMostSteps) {
     e = launch_rows(logprob_reread_kernel<T, 512, kGrad>, a, a.rows, kMaxCluster, 512, 0, stream);
     return e == cudaSuccess ? SEQSUM_OK : note_cuda(e);
   }
   auto kernel = logprob_kernel<T, kGrad>;
   constexpr int kThreads = kWarps * 32 + 32;
-  const size_t shared = shared_bytes<kGrad>(a.steps);
+  const size_t shared = shared_bytes(a.steps);
   int device = 0, most = 0;
   if ((e = cudaGetDevice(&device)) != cudaSuccess) return note_cuda(e);
   if (device < kDevices) most = fits[device][log2][a.steps].load(std::memory_order_relaxed);
   if (most == 0) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared_bytes<kGrad>(kMostSteps<kGrad>));
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared_bytes(kMostSteps));
     if (e == cudaSuccess) e = launch_rows(kernel, a, 1, size, kThreads, shared, stream, &most);
     if (e != cudaSuccess) return note_cuda(e);
     if (most < 1) return SEQSUM_ECUDA;

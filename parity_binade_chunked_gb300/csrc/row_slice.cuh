@@ -1,7 +1,7 @@
-// Rows of logits on chip: a row is read once, in 16-byte vectors, by the
-// CTAs of one thread-block cluster, and stays in their registers while it is
-// reduced.  What the kernels on rows share: element types, the slice of a
-// row that a thread holds, sums over a cluster.
+// Rows of logits on chip: a row is read once, in 16-byte vectors, by the CTAs
+// of one thread-block cluster, and stays there while it is reduced.  What the
+// kernels on rows share: element types, the parts of a row that a CTA or a
+// thread has, what the CTAs of a cluster tell each other, sums over warps.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -215,9 +215,9 @@ __device__ __forceinline__ float warp_add(float v) {   // the same tree in every
 // that stick out of the row are read element by element, so nothing outside
 // the row is touched; what is not in the row is -inf.
 //
-// KV > 0: at most KV steps, kept in registers.  KV = 0: any number of steps,
-// read again from global memory (L2) by every pass.  NT = 32: every warp has a
-// row of its own.
+// KV > 0: at most KV steps, kept in registers (for passes over elements each by
+// itself, and for short rows, one a warp: NT = 32).  KV = 0: any number of
+// steps, read again from global memory (L2) by every pass.
 template <typename T, int KV, int NT>
 struct Slice {
   static constexpr int kE = Elem<T>::kPerVec;
@@ -310,26 +310,29 @@ struct Slice {
 
 // ---- rows streamed through shared memory
 //
-// A cluster takes row after row.  In each of its CTAs one warp (the producer)
-// brings the CTA's slice of each row into the next of a few buffers in shared
-// memory; the other warps make passes over the buffers and leave them one by
-// one.
+// A cluster takes row after row.  In each of its CTAs one warp brings the CTA's
+// slice of each row into the next of a few buffers in shared memory, ahead of
+// the work; all make passes over the buffers and leave them one by one.  So the
+// next row's copy is on its way while this one is summed, and a pass costs no
+// registers: as many CTAs as their buffers allow share an SM and fill each
+// other's waits.
 //
 // A row's 16-byte vectors, counted from the aligned address at or below its
 // first element, go to the lanes of a warp in steps of 32, and the steps are
-// cut into segments as even as can be, one for each warp of the cluster.  The
-// cluster's size goes by the row's length alone, so the same vectors meet in
-// one thread in the same order whatever else a call holds.
+// cut into segments as even as can be, one for each warp of the cluster.
+// Where the cluster's size goes by the row's length alone, the same vectors
+// meet in one thread in the same order whatever else a call holds.
 //
 // What lies inside the row comes by one bulk copy; vectors that stick out of
 // it are put together from elements read one by one, with -inf beside them and
 // after them up to the end of the last step.
 //
-// The CTAs tell each other 8 bytes a segment through `Exchange`: each is
-// written to every CTA, the writes count down a barrier there.  A warp may
-// post a row's segments before it waits for the row before; a post then comes
-// after every warp has left the exchange three rows before, so there are four
-// boxes in turn.
+// The warps tell each other 8-byte words: each is written to every CTA of the
+// cluster with an asynchronous store, and the stores count down a barrier
+// there, so that neither a fence nor a barrier of the whole cluster is needed.
+// A warp may post a word before it waits for the last one; a post then comes
+// after every warp has left the exchange three before, so there are four boxes
+// in turn.
 
 constexpr uint64_t kWaitNs = 2000000000ull;   // waits for copies and for other CTAs give up after 2 s
 
@@ -383,12 +386,10 @@ __device__ __forceinline__ void send(uint2 *to, uint64_t *bar, uint32_t rank, ui
 }
 
 struct Exchange {
-  uint64_t *box;   // one for each segment of the row
+  uint64_t *box;   // one for each warp of the cluster
   uint64_t *bar;
-  uint32_t bytes;
 
-  __device__ __forceinline__ void ready() const { bar_expect(bar, bytes); }   // one thread, for the next time
-  // v (the same in every lane) for segment `at` of the row to every CTA
+  // v (the same in every lane) to box `at` of every CTA
   __device__ __forceinline__ void post(int32_t at, uint64_t v, uint32_t size) const {
     const uint32_t lane = threadIdx.x & 31;
     if (lane < size)
