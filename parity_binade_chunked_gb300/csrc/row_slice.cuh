@@ -423,6 +423,8 @@ struct Stream {
     buf = b;
   }
   __device__ __forceinline__ int32_t index(int32_t vec, int e) const { return (begin + vec) * kE + e - off; }
+  // this lane's vector of a step of the slice
+  __device__ __forceinline__ uint4 vec(int32_t st) const { return buf[st * 32 + (threadIdx.x & 31)]; }
 
   __device__ __forceinline__ bool cut_head() const { return off > 0 && begin == 0 && n > 0; }
   __device__ __forceinline__ bool cut_tail() const { return n > 0 && index(n, 0) > vocab; }
@@ -475,6 +477,34 @@ struct Stream {
 #pragma unroll
     for (int e = 0; e < kE; e++)
       if (vec < n && i + e >= 0 && i + e < vocab) Elem<T>::store(row + i + e, x[e]);
+  }
+};
+
+// A whole row in global memory, seen as a slice: what a CTA that has a row to
+// itself reads again from L2 in every pass.
+template <typename T>
+struct FarRow {
+  static constexpr int kE = Elem<T>::kPerVec;
+  static constexpr int32_t begin = 0;
+  const T *p;
+  int32_t vocab, off, steps;
+  __device__ __forceinline__ void set(const T *row, int32_t v) {
+    p = row;
+    vocab = v;
+    off = (int32_t)((uint32_t)reinterpret_cast<uintptr_t>(row) & 15u) / (int)sizeof(T);
+    steps = (off + v + 32 * kE - 1) / (32 * kE);
+  }
+  __device__ __forceinline__ int32_t step_of(uint32_t share, int log2) const {
+    return (int32_t)(((uint64_t)steps * share) >> log2);
+  }
+  __device__ __forceinline__ int32_t index(int32_t vec, int e) const { return vec * kE + e - off; }
+  __device__ __forceinline__ uint4 vec(int32_t st) const {
+    const int32_t i = index(st * 32 + (int32_t)(threadIdx.x & 31), 0);
+    if (i >= 0 && i + kE <= vocab) return __ldg(reinterpret_cast<const uint4 *>(p + i));
+    float x[kE];
+#pragma unroll
+    for (int e = 0; e < kE; e++) x[e] = i + e >= 0 && i + e < vocab ? Elem<T>::load(p + i + e) : -INFINITY;
+    return Elem<T>::pack(x);
   }
 };
 

@@ -30,6 +30,7 @@
 #include <math.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "../../include/seqsum.h"
 #include "row_slice.cuh"
@@ -374,19 +375,30 @@ __global__ __launch_bounds__(NT) void sample_reread_kernel(const SampleArgs a) {
 // by segments; the place of the token.  The words of a part travel while the
 // next row's first part is worked on.
 
+//
+// Where the rows are many, a CTA takes a row to itself: it reads the row from
+// HBM once and from L2 in the later passes, and tells no one anything.  Twice
+// the SMs' number of rows is under way then, instead of a quarter.
+
+enum Kind { kPlain, kSearch, kFar };   // without top-k and top-p; with them; rows in L2
+
 constexpr int kList = 1280;   // entries that a search can take out of the row
-constexpr int kOwn = 192;     // ... that a warp can of its segment
+constexpr int kFarSteps = 8192;   // of a row that a CTA takes to itself, at most
+template <Kind K>
+constexpr int kOwn = K == kFar ? 384 : 192;   // ... that a warp can of its segment
+template <Kind K>
+constexpr int kMost = K == kFar ? 1 : kMaxCluster;   // CTAs a row at most
 
 // What the CTA's warps share, and what others of the cluster write to.  Calls
 // without top-k and top-p have no use for lists; they get a third buffer.
-template <int W, bool kSearch>
+template <int W, Kind K>
 struct Picks {
-  static constexpr int kBinsHere = kSearch ? kBins : 1, kListHere = kSearch ? kList : 1, kOwnHere = kSearch ? kOwn : 1;
-  static constexpr int kBoxes = kMaxCluster * W;
+  static constexpr int kBinsHere = K != kPlain ? kBins : 1, kListHere = K != kPlain ? kList : 1,
+                       kOwnHere = K != kPlain ? kOwn<K> : 1, kBoxes = kMost<K> * W;
   uint64_t full[3], empty[3], told[4], parts, totals, entries;
   uint64_t box[4][kBoxes];        // a word of every warp of the cluster
-  uint64_t step_mass[32];         // of the segment that the token is in
-  uint4 bins[kBinsHere];          // a split of the CTA's entries: count, and mass in two halves
+  uint64_t step_mass[K == kFar ? kFarSteps / W : 32];   // of the segment that the token is in
+  uint4 bins[kBinsHere];          // a split of the CTA's entries: count, and mass in three parts
   uint4 part[kBinsHere];          // this CTA's share of the bins, of every CTA
   uint4 total[kBinsHere];         // the bins summed over the cluster: count, mass
   uint32_t listed, small_listed;
@@ -395,8 +407,10 @@ struct Picks {
   uint2 own[W][kOwnHere];         // a warp's
 };
 
-template <bool kSearch>
-constexpr int kBuffers = kSearch ? 2 : 3;
+template <Kind K>
+constexpr int kBuffers = K == kFar ? 0 : K == kSearch ? 2 : 3;
+
+__device__ __forceinline__ uint64_t mass_of(uint4 bin) { return bin.y + ((uint64_t)bin.z << 11) + ((uint64_t)bin.w << 22); }
 
 struct Found {
   int bin;                        // -1: the need is not reached
@@ -404,11 +418,12 @@ struct Found {
   uint64_t mass, mass_before;
 };
 
-template <typename T, int W, bool kSearch>
+template <typename T, int W, Kind K>
 struct Picker {
   static constexpr int kE = Elem<T>::kPerVec, kThreads = W * 32;
-  Picks<W, kSearch> &sh;
-  Stream<T> x;
+  static constexpr int kAhead = K == kFar ? 4 : 1;   // steps whose vectors are loaded side by side
+  Picks<W, K> &sh;
+  std::conditional_t<K == kFar, FarRow<T>, Stream<T>> x;
   uint32_t rank, size, posted = 0, heard = 0, totalled = 0, shared_lists = 0;
   int32_t st0, st1;     // this warp's steps
   float m, c;
@@ -419,13 +434,14 @@ struct Picker {
   float own_from = 0.0f;
   int32_t listed = -1;  // entries of sh.all, once a search goes over those; -1: over the row
 
-  __device__ Picker(Picks<W, kSearch> &s) : sh(s) {}
+  __device__ Picker(Picks<W, K> &s) : sh(s) {}
 
   // ---- the CTA's working warps, and the cluster's
 
   __device__ __forceinline__ void team() const { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kThreads) : "memory"); }
   // all of the CTA's working warps go on together or give up together
   __device__ __forceinline__ void agree() {
+    if (K == kFar) return;   // (no waits that could give up)
     uint32_t all;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
@@ -438,6 +454,11 @@ struct Picker {
   // its word after next only once it has waited for this one, so that of four
   // boxes the one that is written is never one that is still read.
   __device__ __forceinline__ void post(uint64_t v) {
+    if (K == kFar) {
+      if ((threadIdx.x & 31) == 0) sh.box[posted & 3][threadIdx.x >> 5] = v;
+      posted++;
+      return;
+    }
     const Exchange e = {sh.box[posted & 3], &sh.told[posted & 3]};
     posted++;
     e.post((int32_t)(rank * W + (threadIdx.x >> 5)), v, size);
@@ -445,13 +466,14 @@ struct Picker {
   __device__ __forceinline__ const uint64_t *hear() {
     const uint32_t b = heard & 3, parity = (heard >> 2) & 1;
     heard++;
+    if (K == kFar) return team(), sh.box[b];
     came &= bar_wait(&sh.told[b], parity);
     if (threadIdx.x == 0) bar_expect(&sh.told[b], size * W * 8);
     return sh.box[b];
   }
   // The sum of the words heard.
   __device__ __forceinline__ uint64_t sum_of(const uint64_t *box) const {
-    constexpr int kPer = (kMaxCluster * W + 31) / 32;
+    constexpr int kPer = (kMost<K> * W + 31) / 32;
     uint64_t sum = 0;
 #pragma unroll
     for (int k = 0; k < kPer; k++) {
@@ -466,10 +488,10 @@ struct Picker {
   // took 1300 to 5000 cycles, reading 256 bins of 8 CTAs 2000.)
   __device__ __forceinline__ void total_bins() {
     team();
-    if (size == 1) {
+    if (K == kFar || size == 1) {
       if (threadIdx.x < kBins) {
         const uint4 v = sh.bins[threadIdx.x];
-        const uint64_t w = v.y + ((uint64_t)v.z << 16);
+        const uint64_t w = mass_of(v);
         sh.total[threadIdx.x] = make_uint4(v.x, (uint32_t)w, (uint32_t)(w >> 32), 0);
       }
       team();
@@ -478,7 +500,7 @@ struct Picker {
     const uint32_t share = kBins / size, to = threadIdx.x / share, bin = threadIdx.x % share, parity = totalled++ & 1;
     if (threadIdx.x < kBins) {
       const uint4 v = sh.bins[threadIdx.x];
-      const uint64_t w = v.y + ((uint64_t)v.z << 16);
+      const uint64_t w = mass_of(v);
       send(&sh.part[rank * share + bin], &sh.parts, to, make_uint4(v.x, (uint32_t)w, (uint32_t)(w >> 32), 0));
     }
     came &= bar_wait(&sh.parts, parity);
@@ -528,8 +550,8 @@ struct Picker {
     const float least = reached_from(from);
     uint2 *to = sh.own[threadIdx.x >> 5];
     int n = 0;
-    for (int32_t st = st0; st < st1 && n <= kOwn; st++) {
-      const uint4 w = x.buf[st * 32 + lane];
+    for (int32_t st = st0; st < st1 && n <= kOwn<K>; st++) {
+      const uint4 w = x.vec(st);
       if (!__any_sync(~0u, Elem<T>::vec_max(w, -INFINITY) >= least)) continue;
       float d[kE];
       octaves(w, d);
@@ -538,12 +560,12 @@ struct Picker {
         const bool in = d[e] >= from && d[e] > kFloor;
         const uint32_t who = __ballot_sync(~0u, in);
         const int at = n + __popc(who & ((1u << lane) - 1));
-        if (in && at < kOwn) to[at] = make_uint2(key_of(d[e]), (uint32_t)x.index(st * 32 + lane, e));
+        if (in && at < kOwn<K>) to[at] = make_uint2(key_of(d[e]), (uint32_t)x.index(st * 32 + lane, e));
         n += __popc(who);
       }
     }
     __syncwarp();
-    own = n <= kOwn ? n : -1;
+    own = n <= kOwn<K> ? n : -1;
     own_from = from;
   }
   // f(octaves, index) of the row's entries from `from` octaves (at least
@@ -560,9 +582,9 @@ struct Picker {
       return;
     }
     const float least = reached_from(from);
-#pragma unroll 1
+#pragma unroll kAhead
     for (int32_t st = st0; st < st1; st++) {
-      const uint4 w = x.buf[st * 32 + lane];
+      const uint4 w = x.vec(st);
       if (Elem<T>::vec_max(w, -INFINITY) >= least) {
         float d[kE];
         octaves(w, d);
@@ -591,9 +613,9 @@ struct Picker {
       return warp_sum(sum);
     }
     const float least = reached_from(from);
-#pragma unroll 1
+#pragma unroll kAhead
     for (int32_t st = st0; st < st1; st++) {
-      const uint4 w = x.buf[st * 32 + lane];
+      const uint4 w = x.vec(st);
       if (Elem<T>::vec_max(w, -INFINITY) >= least) {
         float d[kE];
         octaves(w, d);
@@ -618,8 +640,9 @@ struct Picker {
   __device__ __forceinline__ void put(uint4 *bins, uint32_t bin, float d) const {
     const uint32_t w = weight(d);
     atomicAdd(&bins[bin].x, 1u);
-    atomicAdd(&bins[bin].y, w & 0xffffu);   // a CTA has less than 2^16 entries: the halves' sums fit 32 bits
-    atomicAdd(&bins[bin].z, w >> 16);
+    atomicAdd(&bins[bin].y, w & 0x7ffu);   // (below 2^21 entries the parts' sums fit 32 bits)
+    atomicAdd(&bins[bin].z, w >> 11 & 0x7ffu);
+    atomicAdd(&bins[bin].w, w >> 22);
   }
   // Entries that a search goes on in: keys [lo, hi), or, where that is one
   // key, indices [ilo, ihi) of it.  A first split (scale > 0) is even in
@@ -682,7 +705,7 @@ struct Picker {
       team();
       if (threadIdx.x < kBins) {
         const uint4 v = sh.bins[threadIdx.x];
-        const uint64_t w = v.y + ((uint64_t)v.z << 16);
+        const uint64_t w = mass_of(v);
         sh.total[threadIdx.x] = make_uint4(v.x, (uint32_t)w, (uint32_t)(w >> 32), 0);
       }
       team();
@@ -774,7 +797,7 @@ struct Picker {
     });
     team();
     const uint32_t mine = sh.listed;
-    if (size == 1) {
+    if (K == kFar || size == 1) {
       if (mine <= (uint32_t)kList) {
         for (uint32_t i = threadIdx.x; i < mine; i += kThreads) sh.all[i] = sh.list[i];
         listed = (int32_t)mine;
@@ -806,10 +829,10 @@ struct Picker {
     constexpr int kPer = kBins / 32;
     clear_bins();
     uint64_t mine = 0;
-#pragma unroll 1
+#pragma unroll kAhead
     for (int32_t st = st0; st < st1; st++) {
       float d[kE];
-      octaves(x.buf[st * 32 + lane], d);
+      octaves(x.vec(st), d);
       uint64_t of_vec = 0;
 #pragma unroll
       for (int e = 0; e < kE; e += 2) of_vec += (uint64_t)weight(d[e]) + weight(d[e + 1]);
@@ -992,18 +1015,18 @@ struct Picker {
   }
 };
 
-template <typename T, int W, bool kSearch>
-__global__ __launch_bounds__(W * 32, W == 8 ? 2 : 1) void sample_kernel(const SampleArgs a) {
-  constexpr int kB = kBuffers<kSearch>;
+template <typename T, int W, Kind K>
+__global__ __launch_bounds__(W * 32, W == 8 || K == kFar ? 2 : 1) void sample_kernel(const SampleArgs a) {
+  constexpr int kB = kBuffers<K> > 0 ? kBuffers<K> : 1;
   extern __shared__ uint4 buffers[];   // kB buffers of a.steps steps, and the rest
-  auto &sh = *reinterpret_cast<Picks<W, kSearch> *>(buffers + kB * a.steps * 32);
+  auto &sh = *reinterpret_cast<Picks<W, K> *>(buffers + kBuffers<K> * a.steps * 32);
   constexpr int kE = Elem<T>::kPerVec, kLog2W = W == 16 ? 4 : 3;
   const uint32_t size = cluster_size(), rank = cluster_rank();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t first = blockIdx.x / size, step = gridDim.x / size;
   const uint32_t turns = ((uint32_t)a.rows - first + step - 1) / step;   // (at most one cluster a row)
   const int log2_size = __ffs(size) - 1;
-  if (threadIdx.x == 0) {
+  if (K != kFar && threadIdx.x == 0) {
     for (int b = 0; b < kB; b++) {
       bar_init(&sh.full[b], 2);
       bar_init(&sh.empty[b], W);
@@ -1030,13 +1053,14 @@ __global__ __launch_bounds__(W * 32, W == 8 ? 2 : 1) void sample_kernel(const Sa
   // registers each, and four times the spills.)
   auto row_at = [&](uint32_t it) { return static_cast<const T *>(a.logits) + row_of(it) * a.stride; };
   {
-    Picker<T, W, kSearch> s(sh);
+    Picker<T, W, K> s(sh);
     s.rank = rank, s.size = size;
-    constexpr int kPer = (kMaxCluster * W + 31) / 32;
+    constexpr int kPer = (kMost<K> * W + 31) / 32;
     const uint32_t half = size * W / 2;
     const int log2_segments = log2_size + kLog2W;
     auto place = [&](uint32_t it) {
-      s.x = stream(it);
+      if constexpr (K == kFar) s.x.set(row_at(it), a.vocab);
+      else s.x = stream(it);
       s.st0 = s.x.step_of(rank * W + warp, log2_segments) - s.x.begin / 32;
       s.st1 = s.x.step_of(rank * W + warp + 1, log2_segments) - s.x.begin / 32;
     };
@@ -1050,10 +1074,10 @@ __global__ __launch_bounds__(W * 32, W == 8 ? 2 : 1) void sample_kernel(const Sa
       place(it);
       const bool greedy = !(temperature_of(row_of(it)) > 0.0f);
       const int32_t top_k = top_k_of(row_of(it));
-      s.came &= bar_wait(&sh.full[it % kB], it / kB & 1);
+      if (K != kFar) s.came &= bar_wait(&sh.full[it % kB], it / kB & 1);
       float m = -INFINITY;
 #pragma unroll 4
-      for (int32_t st = s.st0; st < s.st1; st++) m = Elem<T>::vec_max(s.x.buf[st * 32 + lane], m);
+      for (int32_t st = s.st0; st < s.st1; st++) m = Elem<T>::vec_max(s.x.vec(st), m);
       const float of_thread = m;
       m = warp_max_all(m);
       uint32_t beside = ordered(-INFINITY);
@@ -1061,13 +1085,13 @@ __global__ __launch_bounds__(W * 32, W == 8 ? 2 : 1) void sample_kernel(const Sa
         beside = 0xffffffffu;
         for (int32_t st = s.st0; st < s.st1; st++) {
           float v[kE];
-          Elem<T>::unpack(s.x.buf[st * 32 + lane], v);
+          Elem<T>::unpack(s.x.vec(st), v);
 #pragma unroll
           for (int e = 0; e < kE; e++)
             if (v[e] == m) beside = min(beside, (uint32_t)s.x.index(st * 32 + lane, e));
         }
         beside = __reduce_min_sync(~0u, beside);
-      } else if (kSearch && top_k > 0 && top_k < a.vocab) {
+      } else if (K != kPlain && top_k > 0 && top_k < a.vocab) {
         const uint32_t j = ((uint32_t)top_k + half - 1) / half;
         if (j <= 32) {
           uint32_t mine = ordered(of_thread);
@@ -1081,7 +1105,7 @@ __global__ __launch_bounds__(W * 32, W == 8 ? 2 : 1) void sample_kernel(const Sa
       s.post(((uint64_t)beside << 32) | __float_as_uint(m));
     };
 
-    if (warp == 0)
+    if (K != kFar && warp == 0)
       for (uint32_t i = 0; i < kB && i < turns; i++) {
         const Stream<T> x = stream(i);
         x.bring_inner(row_at(i), &sh.full[i]);
@@ -1093,7 +1117,7 @@ __global__ __launch_bounds__(W * 32, W == 8 ? 2 : 1) void sample_kernel(const Sa
       // a row goes where the last one was
       const uint32_t next = it + kB - 1;
       float edge = 0.0f;
-      bool bring = warp == 0 && it > 0 && next < turns;
+      bool bring = K != kFar && warp == 0 && it > 0 && next < turns;
       if (bring) {
         s.came &= bar_wait(&sh.empty[(it - 1) % kB], (it - 1) / kB & 1);
         bring = __all_sync(~0u, s.came);   // (if not, the CTA's next agreement ends it)
@@ -1110,7 +1134,7 @@ __global__ __launch_bounds__(W * 32, W == 8 ? 2 : 1) void sample_kernel(const Sa
       const int32_t top_k = top_k_of(row);
       const float top_p = a.s.top_ps ? a.s.top_ps[row] : a.s.top_p;
       const float min_p = a.s.min_ps ? a.s.min_ps[row] : a.s.min_p;
-      const bool greedy = !(temperature > 0.0f), by_k = kSearch && top_k > 0 && top_k < a.vocab, by_p = kSearch && top_p < 1.0f;
+      const bool greedy = !(temperature > 0.0f), by_k = K != kPlain && top_k > 0 && top_k < a.vocab, by_p = K != kPlain && top_p < 1.0f;
       s.own = -1;
       const uint64_t *box = s.hear();
       uint32_t besides[kPer];
@@ -1147,14 +1171,14 @@ __global__ __launch_bounds__(W * 32, W == 8 ? 2 : 1) void sample_kernel(const Sa
         s.m = m;
         s.c = __fdiv_rn(1.44269504f, temperature);
         s.special = !(m < INFINITY && s.c < INFINITY);
-        if constexpr (kSearch) if (by_k || by_p) {
+        if constexpr (K != kPlain) if (by_k || by_p) {
           float least = kFloor;
           if (by_k) {
             // a number that one warp of each two reaches: half of them
             uint32_t at;
-            if (size * W <= 32) at = max(besides[0], __shfl_xor_sync(~0u, besides[0], half));
-            else if (kPer == 2 || size * W <= 64) at = max(besides[0], besides[1]);
-            else at = min(max(besides[0], besides[kPer / 2]), max(besides[1], besides[kPer - 1]));
+            if (kPer == 1 || size * W <= 32) at = max(besides[0], __shfl_xor_sync(~0u, besides[0], half));
+            else if (kPer == 2 || size * W <= 64) at = max(besides[0], besides[kPer > 1]);
+            else at = min(max(besides[0], besides[kPer / 2]), max(besides[kPer > 1], besides[kPer - 1]));
             if (lane >= (int)half) at = ~0u;
             const float v = from_ordered(__reduce_min_sync(~0u, at));
             if (v > -INFINITY) least = fmaxf(kFloor, v == m ? 0.0f : (v - m) * s.c);   // (fmaxf passes NaN over)
@@ -1168,7 +1192,7 @@ __global__ __launch_bounds__(W * 32, W == 8 ? 2 : 1) void sample_kernel(const Sa
 #pragma unroll 4
           for (int32_t st = s.st0; st < s.st1; st++) {
             float d[kE];
-            s.octaves(s.x.buf[st * 32 + lane], d);
+            s.octaves(s.x.vec(st), d);
             uint64_t of_vec = 0;
 #pragma unroll
             for (int e = 0; e < kE; e += 2) of_vec += (uint64_t)weight(d[e]) + weight(d[e + 1]);   // 0 from kFloor on, and for NaN
@@ -1215,7 +1239,7 @@ __global__ __launch_bounds__(W * 32, W == 8 ? 2 : 1) void sample_kernel(const Sa
           const int32_t first_step = s.x.step_of(owner, log2_segments) - s.x.begin / 32,
                         steps = s.x.step_of(owner + 1, log2_segments) - s.x.begin / 32 - first_step;
           auto weights = [&](int32_t st, float *d, uint32_t *w) {
-            s.octaves(s.x.buf[(first_step + st) * 32 + lane], d);
+            s.octaves(s.x.vec(first_step + st), d);
             uint64_t sum = 0;
 #pragma unroll
             for (int e = 0; e < kE; e++) {
@@ -1231,10 +1255,19 @@ __global__ __launch_bounds__(W * 32, W == 8 ? 2 : 1) void sample_kernel(const Sa
             if (lane == 0) sh.step_mass[st] = sum;
           }
           s.team();
-          const uint64_t of_step = lane < steps ? sh.step_mass[lane] : 0, upto_step = before + warp_scan(of_step, lane);
-          const int32_t st = __ffs(__ballot_sync(~0u, target < upto_step)) - 1;
+          int32_t st = 0;
+          for (int32_t at = 0;; at += 32) {   // (a segment has hardly more than 32 steps)
+            const uint64_t of_step = at + lane < steps ? sh.step_mass[at + lane] : 0, upto_step = before + warp_scan(of_step, lane);
+            const uint32_t past = __ballot_sync(~0u, target < upto_step);
+            if (past || at + 32 >= steps) {
+              const int l = max(0, __ffs(past) - 1);
+              before = __shfl_sync(~0u, upto_step - of_step, l);
+              st = at + l;
+              break;
+            }
+            before = __shfl_sync(~0u, upto_step, 31);
+          }
           if (st % W == warp) {
-            before = __shfl_sync(~0u, upto_step - of_step, st);
             const uint64_t of_vec = weights(st, d, w);
             uint64_t sum = before + warp_scan(of_vec, lane) - of_vec;
 #pragma unroll
@@ -1252,7 +1285,7 @@ __global__ __launch_bounds__(W * 32, W == 8 ? 2 : 1) void sample_kernel(const Sa
         if (!s.ok) break;
       }
       __syncwarp();
-      if (lane == 0) bar_arrive(&sh.empty[it % kB]);
+      if (K != kFar && lane == 0) bar_arrive(&sh.empty[it % kB]);
     }
     if (!s.ok) {
       // a wait gave up: what is not done is marked, copies in flight land before the CTA goes
@@ -1268,22 +1301,22 @@ __global__ __launch_bounds__(W * 32, W == 8 ? 2 : 1) void sample_kernel(const Sa
 
 constexpr int kDevices = 16;   // whose occupancy is kept (for a function, a number of CTAs and a buffer's size)
 
-template <int W, bool kSearch>
-constexpr int kMostSteps = (int)(((226 << 10) - sizeof(Picks<W, kSearch>)) / (kBuffers<kSearch> * 32 * 16));
+template <int W, Kind K>
+constexpr int kMostSteps = K == kFar ? 1 : (int)(((226 << 10) - sizeof(Picks<W, K>)) / ((kBuffers<K> + (K == kFar)) * 32 * 16));
 
-template <typename T, int W, bool kSearch>
+template <typename T, int W, Kind K>
 int run_sample(SampleArgs a, int size, int log2, cudaStream_t stream) {
-  static std::atomic<int> fits[kDevices][4][kMostSteps<W, kSearch> + 1];   // clusters at once, by size and steps (0: not known)
-  auto kernel = sample_kernel<T, W, kSearch>;
+  static std::atomic<int> fits[kDevices][4][kMostSteps<W, K> + 1];   // clusters at once, by size and steps (0: not known)
+  auto kernel = sample_kernel<T, W, K>;
   constexpr int kThreads = W * 32;
-  const size_t shared = (size_t)a.steps * kBuffers<kSearch> * 32 * 16 + sizeof(Picks<W, kSearch>);
+  const size_t shared = (size_t)a.steps * kBuffers<K> * 32 * 16 + sizeof(Picks<W, K>);
   int device = 0, most = 0;
   cudaError_t e = cudaGetDevice(&device);
   if (e != cudaSuccess) return note_cuda(e);
   if (device < kDevices) most = fits[device][log2][a.steps].load(std::memory_order_relaxed);
   if (most == 0) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSteps<W, kSearch> * kBuffers<kSearch> * 32 * 16 +
-                             (int)sizeof(Picks<W, kSearch>));
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSteps<W, K> * kBuffers<K> * 32 * 16 +
+                             (int)sizeof(Picks<W, K>));
     if (e == cudaSuccess) e = launch_rows(kernel, a, 1, size, kThreads, shared, stream, &most);
     if (e != cudaSuccess) return note_cuda(e);
     if (most < 1) return SEQSUM_ECUDA;
@@ -1302,19 +1335,23 @@ int choose_sample(SampleArgs a, cudaStream_t stream) {
   const int64_t vecs = ((int64_t)a.vocab + kE - 1) / kE + 1;   // whatever the alignment
   const int64_t steps = (vecs + 31) / 32;
   const int sms = multiprocessors();
+  if (steps > 66 && steps <= kFarSteps && a.rows * 2 >= sms) {
+    a.steps = 0;
+    return run_sample<T, 16, kFar>(a, 1, 0, stream);
+  }
   int size = 1, log2 = 0;
   while (size < kMaxCluster && (steps > (int64_t)size * 66 || (a.rows * size * 2 <= sms && steps > (int64_t)size * 8)))
     size *= 2, log2++;
   a.steps = (int32_t)((steps + size - 1) / size);
   // (three buffers where there is room for them)
-  const bool search = a.s.top_ks || a.s.top_ps || a.s.top_k > 0 || a.s.top_p < 1.0f || a.steps > kMostSteps<16, false>;
-  if (a.steps > kMostSteps<16, true>) {
+  const bool search = a.s.top_ks || a.s.top_ps || a.s.top_k > 0 || a.s.top_p < 1.0f || a.steps > kMostSteps<16, kPlain>;
+  if (a.steps > kMostSteps<16, kSearch>) {
     const cudaError_t e = launch_rows(sample_reread_kernel<T, 512>, a, a.rows, kMaxCluster, 512, 0, stream);
     return e == cudaSuccess ? SEQSUM_OK : note_cuda(e);
   }
   // (one CTA an SM from 66 steps on: then twice the warps)
-  if (search) return a.steps > 66 ? run_sample<T, 16, true>(a, size, log2, stream) : run_sample<T, 8, true>(a, size, log2, stream);
-  return a.steps > 66 ? run_sample<T, 16, false>(a, size, log2, stream) : run_sample<T, 8, false>(a, size, log2, stream);
+  if (search) return a.steps > 66 ? run_sample<T, 16, kSearch>(a, size, log2, stream) : run_sample<T, 8, kSearch>(a, size, log2, stream);
+  return a.steps > 66 ? run_sample<T, 16, kPlain>(a, size, log2, stream) : run_sample<T, 8, kPlain>(a, size, log2, stream);
 }
 
 }  // namespace
