@@ -383,6 +383,7 @@ __global__ __launch_bounds__(NT) void sample_reread_kernel(const SampleArgs a) {
 enum Kind { kPlain, kSearch, kFar };   // without top-k and top-p; with them; rows in L2
 
 constexpr int kList = 1280;   // entries that a search can take out of the row
+constexpr int kFarWarps = 16, kFarCtas = 2;
 constexpr int kFarSteps = 8192;   // of a row that a CTA takes to itself, at most
 template <Kind K>
 constexpr int kOwn = K == kFar ? 384 : 192;   // ... that a warp can of its segment
@@ -421,7 +422,7 @@ struct Found {
 template <typename T, int W, Kind K>
 struct Picker {
   static constexpr int kE = Elem<T>::kPerVec, kThreads = W * 32;
-  static constexpr int kAhead = K == kFar ? 4 : 1;   // steps whose vectors are loaded side by side
+  static constexpr int kAhead = 4;   // steps of far rows whose vectors are loaded side by side
   Picks<W, K> &sh;
   std::conditional_t<K == kFar, FarRow<T>, Stream<T>> x;
   uint32_t rank, size, posted = 0, heard = 0, totalled = 0, shared_lists = 0;
@@ -538,6 +539,30 @@ struct Picker {
       for (int e = 0; e < kE; e += 2) split(mul2(add2(pair(d[e], d[e + 1]), mm), cc), d[e], d[e + 1]);
     }
   }
+  // f(step, this lane's vector of it) for the warp's steps; of far rows some
+  // vectors are loaded side by side
+  template <typename F>
+  __device__ __forceinline__ void steps(F f) const {
+    if constexpr (K == kFar) {
+      for (int32_t st = st0; st < st1; st += kAhead) {
+        uint4 w[kAhead];
+        if (st + kAhead <= st1 && x.index(st * 32, 0) >= 0 && x.index((st + kAhead) * 32, 0) <= x.vocab) {
+          const uint4 *p = reinterpret_cast<const uint4 *>(x.p + x.index(st * 32 + (int32_t)(threadIdx.x & 31), 0));
+#pragma unroll
+          for (int k = 0; k < kAhead; k++) w[k] = __ldg(p + 32 * k);
+        } else {
+          constexpr uint32_t ninf = Elem<T>::kNegInf;
+#pragma unroll
+          for (int k = 0; k < kAhead; k++) w[k] = st + k < st1 ? x.vec(st + k) : make_uint4(ninf, ninf, ninf, ninf);
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; k++) f(st + k, w[k]);
+      }
+    } else {
+#pragma unroll 1
+      for (int32_t st = st0; st < st1; st++) f(st, x.vec(st));
+    }
+  }
   // a logit that entries from `from` octaves on reach, with room for roundings
   __device__ __forceinline__ float reached_from(float from) const {
     const float v = m + __fdiv_rn(from, c) * 1.00001f, t = v - (fabsf(v) + fabsf(m)) * 1e-6f;
@@ -550,9 +575,8 @@ struct Picker {
     const float least = reached_from(from);
     uint2 *to = sh.own[threadIdx.x >> 5];
     int n = 0;
-    for (int32_t st = st0; st < st1 && n <= kOwn<K>; st++) {
-      const uint4 w = x.vec(st);
-      if (!__any_sync(~0u, Elem<T>::vec_max(w, -INFINITY) >= least)) continue;
+    steps([&](int32_t st, uint4 w) {
+      if (n > kOwn<K> || !__any_sync(~0u, Elem<T>::vec_max(w, -INFINITY) >= least)) return;
       float d[kE];
       octaves(w, d);
 #pragma unroll
@@ -563,7 +587,7 @@ struct Picker {
         if (in && at < kOwn<K>) to[at] = make_uint2(key_of(d[e]), (uint32_t)x.index(st * 32 + lane, e));
         n += __popc(who);
       }
-    }
+    });
     __syncwarp();
     own = n <= kOwn<K> ? n : -1;
     own_from = from;
@@ -582,22 +606,19 @@ struct Picker {
       return;
     }
     const float least = reached_from(from);
-#pragma unroll kAhead
-    for (int32_t st = st0; st < st1; st++) {
-      const uint4 w = x.vec(st);
-      if (Elem<T>::vec_max(w, -INFINITY) >= least) {
-        float d[kE];
-        octaves(w, d);
-        bool any = false;
+    steps([&](int32_t st, uint4 w) {
+      if (!(Elem<T>::vec_max(w, -INFINITY) >= least)) return;
+      float d[kE];
+      octaves(w, d);
+      bool any = false;
 #pragma unroll
-        for (int e = 0; e < kE; e++) any |= d[e] >= from && d[e] <= to;
-        if (any) {
+      for (int e = 0; e < kE; e++) any |= d[e] >= from && d[e] <= to;
+      if (any) {
 #pragma unroll
-          for (int e = 0; e < kE; e++)
-            if (d[e] >= from && d[e] <= to && d[e] > kFloor) f(d[e], x.index(st * 32 + lane, e));
-        }
+        for (int e = 0; e < kE; e++)
+          if (d[e] >= from && d[e] <= to && d[e] > kFloor) f(d[e], x.index(st * 32 + lane, e));
       }
-    }
+    });
   }
   // The sum of g(octaves, index) over them, where g is 0 for NaN and -inf
   // (without branches: for rows of which many entries count).
@@ -613,17 +634,14 @@ struct Picker {
       return warp_sum(sum);
     }
     const float least = reached_from(from);
-#pragma unroll kAhead
-    for (int32_t st = st0; st < st1; st++) {
-      const uint4 w = x.vec(st);
-      if (Elem<T>::vec_max(w, -INFINITY) >= least) {
-        float d[kE];
-        octaves(w, d);
+    steps([&](int32_t st, uint4 w) {
+      if (!(Elem<T>::vec_max(w, -INFINITY) >= least)) return;
+      float d[kE];
+      octaves(w, d);
 #pragma unroll
-        for (int e = 0; e < kE; e += 2)
-          sum += (uint64_t)g(d[e], x.index(st * 32 + lane, e)) + g(d[e + 1], x.index(st * 32 + lane, e + 1));
-      }
-    }
+      for (int e = 0; e < kE; e += 2)
+        sum += (uint64_t)g(d[e], x.index(st * 32 + lane, e)) + g(d[e + 1], x.index(st * 32 + lane, e + 1));
+    });
     return warp_sum(sum);
   }
   // ... or of the list
@@ -829,16 +847,15 @@ struct Picker {
     constexpr int kPer = kBins / 32;
     clear_bins();
     uint64_t mine = 0;
-#pragma unroll kAhead
-    for (int32_t st = st0; st < st1; st++) {
+    steps([&](int32_t, uint4 v) {
       float d[kE];
-      octaves(x.vec(st), d);
+      octaves(v, d);
       uint64_t of_vec = 0;
 #pragma unroll
       for (int e = 0; e < kE; e += 2) of_vec += (uint64_t)weight(d[e]) + weight(d[e + 1]);
       mine += of_vec;
       if (d[0] > kFloor) atomicAdd(&sh.bins[(int)(-d[0] * 8.0f)].x, 1u);
-    }
+    });
     post(warp_sum(mine));
     total_bins();
     const uint64_t all = max((uint64_t)1, sum_of(hear())), cut = max((uint64_t)1, share(part_of(top_p), all));
@@ -1016,11 +1033,11 @@ struct Picker {
 };
 
 template <typename T, int W, Kind K>
-__global__ __launch_bounds__(W * 32, W == 8 || K == kFar ? 2 : 1) void sample_kernel(const SampleArgs a) {
+__global__ __launch_bounds__(W * 32, K == kFar ? kFarCtas : W == 8 ? 2 : 1) void sample_kernel(const SampleArgs a) {
   constexpr int kB = kBuffers<K> > 0 ? kBuffers<K> : 1;
   extern __shared__ uint4 buffers[];   // kB buffers of a.steps steps, and the rest
   auto &sh = *reinterpret_cast<Picks<W, K> *>(buffers + kBuffers<K> * a.steps * 32);
-  constexpr int kE = Elem<T>::kPerVec, kLog2W = W == 16 ? 4 : 3;
+  constexpr int kE = Elem<T>::kPerVec, kLog2W = W == 32 ? 5 : W == 16 ? 4 : 3;
   const uint32_t size = cluster_size(), rank = cluster_rank();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t first = blockIdx.x / size, step = gridDim.x / size;
@@ -1076,20 +1093,19 @@ __global__ __launch_bounds__(W * 32, W == 8 || K == kFar ? 2 : 1) void sample_ke
       const int32_t top_k = top_k_of(row_of(it));
       if (K != kFar) s.came &= bar_wait(&sh.full[it % kB], it / kB & 1);
       float m = -INFINITY;
-#pragma unroll 4
-      for (int32_t st = s.st0; st < s.st1; st++) m = Elem<T>::vec_max(s.x.vec(st), m);
+      s.steps([&](int32_t, uint4 v) { m = Elem<T>::vec_max(v, m); });
       const float of_thread = m;
       m = warp_max_all(m);
       uint32_t beside = ordered(-INFINITY);
       if (greedy) {
         beside = 0xffffffffu;
-        for (int32_t st = s.st0; st < s.st1; st++) {
+        s.steps([&](int32_t st, uint4 w) {
           float v[kE];
-          Elem<T>::unpack(s.x.vec(st), v);
+          Elem<T>::unpack(w, v);
 #pragma unroll
           for (int e = 0; e < kE; e++)
             if (v[e] == m) beside = min(beside, (uint32_t)s.x.index(st * 32 + lane, e));
-        }
+        });
         beside = __reduce_min_sync(~0u, beside);
       } else if (K != kPlain && top_k > 0 && top_k < a.vocab) {
         const uint32_t j = ((uint32_t)top_k + half - 1) / half;
@@ -1189,15 +1205,14 @@ __global__ __launch_bounds__(W * 32, W == 8 || K == kFar ? 2 : 1) void sample_ke
         uint64_t mine;
         if (!by_k && !by_p && floor_w == 0) {
           mine = 0;
-#pragma unroll 4
-          for (int32_t st = s.st0; st < s.st1; st++) {
+          s.steps([&](int32_t, uint4 v) {
             float d[kE];
-            s.octaves(s.x.vec(st), d);
+            s.octaves(v, d);
             uint64_t of_vec = 0;
 #pragma unroll
             for (int e = 0; e < kE; e += 2) of_vec += (uint64_t)weight(d[e]) + weight(d[e + 1]);   // 0 from kFloor on, and for NaN
             mine += of_vec;
-          }
+          });
           mine = warp_sum(mine);
         } else {
           mine = s.row_sum(fmaxf(kFloor, -__uint_as_float(end.key)), kept);
@@ -1337,7 +1352,7 @@ int choose_sample(SampleArgs a, cudaStream_t stream) {
   const int sms = multiprocessors();
   if (steps > 66 && steps <= kFarSteps && a.rows * 2 >= sms) {
     a.steps = 0;
-    return run_sample<T, 16, kFar>(a, 1, 0, stream);
+    return run_sample<T, kFarWarps, kFar>(a, 1, 0, stream);
   }
   int size = 1, log2 = 0;
   while (size < kMaxCluster && (steps > (int64_t)size * 66 || (a.rows * size * 2 <= sms && steps > (int64_t)size * 8)))
