@@ -20,13 +20,14 @@
 // every fourth or eighth entry, says which eighths the cut is in; their entries
 // are split, with the exact mass before them, which confirms the estimate.
 //
-// What bounds it is not HBM (256 x 131072 bf16: floor 9.9 us; plain 38 us, top-k
-// 50 118 us, top-p 0.9 180 us; 512 x 131072 fp32 plain 134 us, floor 40) but the
-// chain of a row's parts: some 8 without filters, 20 with, each a pass over a
-// warp's 8 steps or a wait for the cluster of about 1000 cycles.  Two CTAs an SM
-// (of 8 warps, 66 KB of buffers each) overlap two rows; a second one made a
-// batch 1.7 times as fast, a third (with one buffer and fewer registers) no
-// faster.
+// What bounds it is not HBM but, where the rows are few, the chain of a row's
+// parts: some 8 without filters, 20 with, each a pass over a warp's steps or a
+// wait for the cluster of about 1000 cycles (one row of 32000 bf16 numbers 6 and
+// 13 us); where they are many, issue slots and the latency of L2: an element
+// costs some 10 instructions a pass and there are two passes without filters,
+// four with.  256 x 131072 bf16 (floor 9.9 us): plain 24 us, top-k 50 42 us,
+// top-p 0.9 95 us, and 193 us at temperature 1.5, where the kept are 40000 of a
+// row and pass the lists; 512 x 131072 fp32 plain 80 us (floor 40).
 #include <math.h>
 
 #include <atomic>
@@ -378,27 +379,30 @@ __global__ __launch_bounds__(NT) void sample_reread_kernel(const SampleArgs a) {
 //
 // Where the rows are many, a CTA takes a row to itself: it reads the row from
 // HBM once and from L2 in the later passes, and tells no one anything.  Twice
-// the SMs' number of rows is under way then, instead of a quarter.
+// the SMs' number of rows is under way then, instead of a quarter (256 x 131072
+// bf16 with top-p 0.9: 95 us, by clusters 180; 64 rows 52 by clusters).
 
-enum Kind { kPlain, kSearch, kFar };   // without top-k and top-p; with them; rows in L2
+// without top-k and top-p, and with them; rows on chip, and in L2
+enum Kind { kPlain, kSearch, kFarPlain, kFarSearch };
+__host__ __device__ constexpr bool is_far(Kind k) { return k >= kFarPlain; }
+__host__ __device__ constexpr bool searches(Kind k) { return k == kSearch || k == kFarSearch; }
 
 constexpr int kList = 1280;   // entries that a search can take out of the row
-constexpr int kFarWarps = 16, kFarCtas = 2;
 constexpr int kFarSteps = 8192;   // of a row that a CTA takes to itself, at most
 template <Kind K>
-constexpr int kOwn = K == kFar ? 384 : 192;   // ... that a warp can of its segment
+constexpr int kOwn = is_far(K) ? 384 : 192;   // ... that a warp can of its segment
 template <Kind K>
-constexpr int kMost = K == kFar ? 1 : kMaxCluster;   // CTAs a row at most
+constexpr int kMost = is_far(K) ? 1 : kMaxCluster;   // CTAs a row at most
 
 // What the CTA's warps share, and what others of the cluster write to.  Calls
 // without top-k and top-p have no use for lists; they get a third buffer.
 template <int W, Kind K>
 struct Picks {
-  static constexpr int kBinsHere = K != kPlain ? kBins : 1, kListHere = K != kPlain ? kList : 1,
-                       kOwnHere = K != kPlain ? kOwn<K> : 1, kBoxes = kMost<K> * W;
+  static constexpr int kBinsHere = searches(K) ? kBins : 1, kListHere = searches(K) ? kList : 1,
+                       kOwnHere = searches(K) ? kOwn<K> : 1, kBoxes = kMost<K> * W;
   uint64_t full[3], empty[3], told[4], parts, totals, entries;
   uint64_t box[4][kBoxes];        // a word of every warp of the cluster
-  uint64_t step_mass[K == kFar ? kFarSteps / W : 32];   // of the segment that the token is in
+  uint64_t step_mass[is_far(K) ? kFarSteps / W : 32];   // of the segment that the token is in
   uint4 bins[kBinsHere];          // a split of the CTA's entries: count, and mass in three parts
   uint4 part[kBinsHere];          // this CTA's share of the bins, of every CTA
   uint4 total[kBinsHere];         // the bins summed over the cluster: count, mass
@@ -409,7 +413,7 @@ struct Picks {
 };
 
 template <Kind K>
-constexpr int kBuffers = K == kFar ? 0 : K == kSearch ? 2 : 3;
+constexpr int kBuffers = is_far(K) ? 0 : searches(K) ? 2 : 3;
 
 __device__ __forceinline__ uint64_t mass_of(uint4 bin) { return bin.y + ((uint64_t)bin.z << 11) + ((uint64_t)bin.w << 22); }
 
@@ -424,7 +428,7 @@ struct Picker {
   static constexpr int kE = Elem<T>::kPerVec, kThreads = W * 32;
   static constexpr int kAhead = 4;   // steps of far rows whose vectors are loaded side by side
   Picks<W, K> &sh;
-  std::conditional_t<K == kFar, FarRow<T>, Stream<T>> x;
+  std::conditional_t<is_far(K), FarRow<T>, Stream<T>> x;
   uint32_t rank, size, posted = 0, heard = 0, totalled = 0, shared_lists = 0;
   int32_t st0, st1;     // this warp's steps
   float m, c;
@@ -442,7 +446,7 @@ struct Picker {
   __device__ __forceinline__ void team() const { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kThreads) : "memory"); }
   // all of the CTA's working warps go on together or give up together
   __device__ __forceinline__ void agree() {
-    if (K == kFar) return;   // (no waits that could give up)
+    if (is_far(K)) return;   // (no waits that could give up)
     uint32_t all;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
@@ -455,7 +459,7 @@ struct Picker {
   // its word after next only once it has waited for this one, so that of four
   // boxes the one that is written is never one that is still read.
   __device__ __forceinline__ void post(uint64_t v) {
-    if (K == kFar) {
+    if (is_far(K)) {
       if ((threadIdx.x & 31) == 0) sh.box[posted & 3][threadIdx.x >> 5] = v;
       posted++;
       return;
@@ -467,7 +471,7 @@ struct Picker {
   __device__ __forceinline__ const uint64_t *hear() {
     const uint32_t b = heard & 3, parity = (heard >> 2) & 1;
     heard++;
-    if (K == kFar) return team(), sh.box[b];
+    if (is_far(K)) return team(), sh.box[b];
     came &= bar_wait(&sh.told[b], parity);
     if (threadIdx.x == 0) bar_expect(&sh.told[b], size * W * 8);
     return sh.box[b];
@@ -489,7 +493,7 @@ struct Picker {
   // took 1300 to 5000 cycles, reading 256 bins of 8 CTAs 2000.)
   __device__ __forceinline__ void total_bins() {
     team();
-    if (K == kFar || size == 1) {
+    if (is_far(K) || size == 1) {
       if (threadIdx.x < kBins) {
         const uint4 v = sh.bins[threadIdx.x];
         const uint64_t w = mass_of(v);
@@ -543,7 +547,7 @@ struct Picker {
   // vectors are loaded side by side
   template <typename F>
   __device__ __forceinline__ void steps(F f) const {
-    if constexpr (K == kFar) {
+    if constexpr (is_far(K)) {
       for (int32_t st = st0; st < st1; st += kAhead) {
         uint4 w[kAhead];
         if (st + kAhead <= st1 && x.index(st * 32, 0) >= 0 && x.index((st + kAhead) * 32, 0) <= x.vocab) {
@@ -815,7 +819,7 @@ struct Picker {
     });
     team();
     const uint32_t mine = sh.listed;
-    if (K == kFar || size == 1) {
+    if (is_far(K) || size == 1) {
       if (mine <= (uint32_t)kList) {
         for (uint32_t i = threadIdx.x; i < mine; i += kThreads) sh.all[i] = sh.list[i];
         listed = (int32_t)mine;
@@ -1033,7 +1037,7 @@ struct Picker {
 };
 
 template <typename T, int W, Kind K>
-__global__ __launch_bounds__(W * 32, K == kFar ? kFarCtas : W == 8 ? 2 : 1) void sample_kernel(const SampleArgs a) {
+__global__ __launch_bounds__(W * 32, W == 8 || K == kFarSearch || (K == kFarPlain && W == 16) ? 2 : 1) void sample_kernel(const SampleArgs a) {
   constexpr int kB = kBuffers<K> > 0 ? kBuffers<K> : 1;
   extern __shared__ uint4 buffers[];   // kB buffers of a.steps steps, and the rest
   auto &sh = *reinterpret_cast<Picks<W, K> *>(buffers + kBuffers<K> * a.steps * 32);
@@ -1043,7 +1047,7 @@ __global__ __launch_bounds__(W * 32, K == kFar ? kFarCtas : W == 8 ? 2 : 1) void
   const uint32_t first = blockIdx.x / size, step = gridDim.x / size;
   const uint32_t turns = ((uint32_t)a.rows - first + step - 1) / step;   // (at most one cluster a row)
   const int log2_size = __ffs(size) - 1;
-  if (K != kFar && threadIdx.x == 0) {
+  if (!is_far(K) && threadIdx.x == 0) {
     for (int b = 0; b < kB; b++) {
       bar_init(&sh.full[b], 2);
       bar_init(&sh.empty[b], W);
@@ -1076,7 +1080,7 @@ __global__ __launch_bounds__(W * 32, K == kFar ? kFarCtas : W == 8 ? 2 : 1) void
     const uint32_t half = size * W / 2;
     const int log2_segments = log2_size + kLog2W;
     auto place = [&](uint32_t it) {
-      if constexpr (K == kFar) s.x.set(row_at(it), a.vocab);
+      if constexpr (is_far(K)) s.x.set(row_at(it), a.vocab);
       else s.x = stream(it);
       s.st0 = s.x.step_of(rank * W + warp, log2_segments) - s.x.begin / 32;
       s.st1 = s.x.step_of(rank * W + warp + 1, log2_segments) - s.x.begin / 32;
@@ -1091,7 +1095,7 @@ __global__ __launch_bounds__(W * 32, K == kFar ? kFarCtas : W == 8 ? 2 : 1) void
       place(it);
       const bool greedy = !(temperature_of(row_of(it)) > 0.0f);
       const int32_t top_k = top_k_of(row_of(it));
-      if (K != kFar) s.came &= bar_wait(&sh.full[it % kB], it / kB & 1);
+      if (!is_far(K)) s.came &= bar_wait(&sh.full[it % kB], it / kB & 1);
       float m = -INFINITY;
       s.steps([&](int32_t, uint4 v) { m = Elem<T>::vec_max(v, m); });
       const float of_thread = m;
@@ -1107,7 +1111,7 @@ __global__ __launch_bounds__(W * 32, K == kFar ? kFarCtas : W == 8 ? 2 : 1) void
             if (v[e] == m) beside = min(beside, (uint32_t)s.x.index(st * 32 + lane, e));
         });
         beside = __reduce_min_sync(~0u, beside);
-      } else if (K != kPlain && top_k > 0 && top_k < a.vocab) {
+      } else if (searches(K) && top_k > 0 && top_k < a.vocab) {
         const uint32_t j = ((uint32_t)top_k + half - 1) / half;
         if (j <= 32) {
           uint32_t mine = ordered(of_thread);
@@ -1121,7 +1125,7 @@ __global__ __launch_bounds__(W * 32, K == kFar ? kFarCtas : W == 8 ? 2 : 1) void
       s.post(((uint64_t)beside << 32) | __float_as_uint(m));
     };
 
-    if (K != kFar && warp == 0)
+    if (!is_far(K) && warp == 0)
       for (uint32_t i = 0; i < kB && i < turns; i++) {
         const Stream<T> x = stream(i);
         x.bring_inner(row_at(i), &sh.full[i]);
@@ -1133,7 +1137,7 @@ __global__ __launch_bounds__(W * 32, K == kFar ? kFarCtas : W == 8 ? 2 : 1) void
       // a row goes where the last one was
       const uint32_t next = it + kB - 1;
       float edge = 0.0f;
-      bool bring = K != kFar && warp == 0 && it > 0 && next < turns;
+      bool bring = !is_far(K) && warp == 0 && it > 0 && next < turns;
       if (bring) {
         s.came &= bar_wait(&sh.empty[(it - 1) % kB], (it - 1) / kB & 1);
         bring = __all_sync(~0u, s.came);   // (if not, the CTA's next agreement ends it)
@@ -1150,7 +1154,7 @@ __global__ __launch_bounds__(W * 32, K == kFar ? kFarCtas : W == 8 ? 2 : 1) void
       const int32_t top_k = top_k_of(row);
       const float top_p = a.s.top_ps ? a.s.top_ps[row] : a.s.top_p;
       const float min_p = a.s.min_ps ? a.s.min_ps[row] : a.s.min_p;
-      const bool greedy = !(temperature > 0.0f), by_k = K != kPlain && top_k > 0 && top_k < a.vocab, by_p = K != kPlain && top_p < 1.0f;
+      const bool greedy = !(temperature > 0.0f), by_k = searches(K) && top_k > 0 && top_k < a.vocab, by_p = searches(K) && top_p < 1.0f;
       s.own = -1;
       const uint64_t *box = s.hear();
       uint32_t besides[kPer];
@@ -1187,7 +1191,7 @@ __global__ __launch_bounds__(W * 32, K == kFar ? kFarCtas : W == 8 ? 2 : 1) void
         s.m = m;
         s.c = __fdiv_rn(1.44269504f, temperature);
         s.special = !(m < INFINITY && s.c < INFINITY);
-        if constexpr (K != kPlain) if (by_k || by_p) {
+        if constexpr (searches(K)) if (by_k || by_p) {
           float least = kFloor;
           if (by_k) {
             // a number that one warp of each two reaches: half of them
@@ -1300,7 +1304,7 @@ __global__ __launch_bounds__(W * 32, K == kFar ? kFarCtas : W == 8 ? 2 : 1) void
         if (!s.ok) break;
       }
       __syncwarp();
-      if (K != kFar && lane == 0) bar_arrive(&sh.empty[it % kB]);
+      if (!is_far(K) && lane == 0) bar_arrive(&sh.empty[it % kB]);
     }
     if (!s.ok) {
       // a wait gave up: what is not done is marked, copies in flight land before the CTA goes
@@ -1317,7 +1321,7 @@ __global__ __launch_bounds__(W * 32, K == kFar ? kFarCtas : W == 8 ? 2 : 1) void
 constexpr int kDevices = 16;   // whose occupancy is kept (for a function, a number of CTAs and a buffer's size)
 
 template <int W, Kind K>
-constexpr int kMostSteps = K == kFar ? 1 : (int)(((226 << 10) - sizeof(Picks<W, K>)) / ((kBuffers<K> + (K == kFar)) * 32 * 16));
+constexpr int kMostSteps = is_far(K) ? 1 : (int)(((226 << 10) - sizeof(Picks<W, K>)) / ((kBuffers<K> + (is_far(K))) * 32 * 16));
 
 template <typename T, int W, Kind K>
 int run_sample(SampleArgs a, int size, int log2, cudaStream_t stream) {
@@ -1341,25 +1345,30 @@ int run_sample(SampleArgs a, int size, int log2, cudaStream_t stream) {
   return e == cudaSuccess ? SEQSUM_OK : note_cuda(e);
 }
 
-// CTAs a row: enough for two of them to share an SM (66 steps a CTA), more
-// where the rows are few; one row of 131072 bf16 numbers takes 17 us with top-p.
-// The tokens do not depend on it: all sums are of integers.
+// CTAs a row: one, reading far, from half the SMs' number of rows on; else
+// enough for two of them to share an SM (66 steps a CTA), more where the rows
+// are few.  The tokens do not depend on it: all sums are of integers.
 template <typename T>
 int choose_sample(SampleArgs a, cudaStream_t stream) {
   constexpr int kE = Elem<T>::kPerVec;
   const int64_t vecs = ((int64_t)a.vocab + kE - 1) / kE + 1;   // whatever the alignment
   const int64_t steps = (vecs + 31) / 32;
   const int sms = multiprocessors();
+  bool search = a.s.top_ks || a.s.top_ps || a.s.top_k > 0 || a.s.top_p < 1.0f;
   if (steps > 66 && steps <= kFarSteps && a.rows * 2 >= sms) {
     a.steps = 0;
-    return run_sample<T, kFarWarps, kFar>(a, 1, 0, stream);
+    if (search) return run_sample<T, 16, kFarSearch>(a, 1, 0, stream);
+    // One row an SM where two of each would not stay in L2 (96 of its 129 MB):
+    // 512 x 131072 fp32 80 us, two an SM 96; 256 x 131072 bf16 26 and 24.
+    return vecs * 16 * 2 * sms > 96 << 20 ? run_sample<T, 32, kFarPlain>(a, 1, 0, stream)
+                                          : run_sample<T, 16, kFarPlain>(a, 1, 0, stream);
   }
   int size = 1, log2 = 0;
   while (size < kMaxCluster && (steps > (int64_t)size * 66 || (a.rows * size * 2 <= sms && steps > (int64_t)size * 8)))
     size *= 2, log2++;
   a.steps = (int32_t)((steps + size - 1) / size);
   // (three buffers where there is room for them)
-  const bool search = a.s.top_ks || a.s.top_ps || a.s.top_k > 0 || a.s.top_p < 1.0f || a.steps > kMostSteps<16, kPlain>;
+  search |= a.steps > kMostSteps<16, kPlain>;
   if (a.steps > kMostSteps<16, kSearch>) {
     const cudaError_t e = launch_rows(sample_reread_kernel<T, 512>, a, a.rows, kMaxCluster, 512, 0, stream);
     return e == cudaSuccess ? SEQSUM_OK : note_cuda(e);
