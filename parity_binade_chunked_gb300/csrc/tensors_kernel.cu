@@ -164,18 +164,23 @@ __device__ __noinline__ double thread_squares_wide(const Chunk &c) {
   return s;
 }
 
-// (Only thread 0 converts and adds in double: with all threads' conversions the
-// fp64 pipe was 70% busy, and the norm of 658 MB took 123 us.)
+// Adds a chunk's squares to `to`, in thread 0.  (Only there anything is
+// converted to double: with all threads' conversions the fp64 pipe was 70%
+// busy, and the norm of 658 MB took 123 us.)
 template <typename F>
-__device__ __forceinline__ double chunk_squares(const Chunk &c, uint4 *v, BlockSum<float> &sum, BlockSum<double> &wide, F next) {
+__device__ __forceinline__ void add_squares(double &to, const Chunk &c, uint4 *v, BlockSum<float> &sum, BlockSum<double> &wide, F next) {
   const float s = sum(c.type == SEQSUM_FP32   ? thread_squares<float>(c, v, next)
                       : c.type == SEQSUM_FP16 ? thread_squares<__half>(c, v, next)
                                               : thread_squares<__nv_bfloat16>(c, v, next));
   // below 2^-80 squares that left fp32's range could count; above all of it, the sum did
-  if (s >= 8.2718061e-25f && s < INFINITY) return threadIdx.x == 0 ? (double)s : 0.0;
-  return wide(c.type == SEQSUM_FP32   ? thread_squares_wide<float>(c)
-              : c.type == SEQSUM_FP16 ? thread_squares_wide<__half>(c)
-                                      : thread_squares_wide<__nv_bfloat16>(c));
+  if (s >= 8.2718061e-25f && s < INFINITY) {
+    if (threadIdx.x == 0) to += (double)s;
+    return;
+  }
+  const double w = wide(c.type == SEQSUM_FP32   ? thread_squares_wide<float>(c)
+                        : c.type == SEQSUM_FP16 ? thread_squares_wide<__half>(c)
+                                                : thread_squares_wide<__nv_bfloat16>(c));
+  if (threadIdx.x == 0) to += w;
 }
 
 // The norm, and the factor of the clipped numbers (NaN stays).
@@ -187,7 +192,7 @@ __device__ __forceinline__ float factor_of(const TensorsArgs &a, float norm) {
   return (q > 1.0f ? 1.0f : q) * a.scale;
 }
 
-// Bound by HBM: 103 us for 658 MB of bf16 in 243 tensors (94% of the measured
+// Bound by HBM: 102 us for 658 MB of bf16 in 243 tensors (95% of the measured
 // copy rate), 348 us for 2.46 GB.  Three CTAs of 256 threads with 128 bytes a
 // thread on the way hold 96 KB of loads an SM; the loads of the next chunk are
 // out before the sum of this one goes through the CTA (without that 119 us).
@@ -212,16 +217,13 @@ __global__ __launch_bounds__(kThreads, kCtas) void norm_kernel(const TensorsArgs
     Chunk after = c;
     if (g < a.ngroups) after = a.chunks[i];
     // the next chunk's numbers are on their way while this one's sum goes through the CTA
-    const double squares = chunk_squares(c, v, sum, wide, [&] {
+    add_squares(s, c, v, sum, wide, [&] {
       if (g < a.ngroups) load_eight(after, 0, v);
     });
     c = after;
-    if (threadIdx.x == 0) {
-      s += squares;
-      if (g != of) {
-        a.parts[of] = s;
-        s = 0.0;
-      }
+    if (g != of && threadIdx.x == 0) {
+      a.parts[of] = s;
+      s = 0.0;
     }
   }
   // (a kernel that depends on this one, and waits for its end, may come onto the SM)
@@ -369,7 +371,8 @@ __global__ __launch_bounds__(kThreads, 1) void short_kernel(const TensorsArgs a)
     const Chunk c = a.chunks[i];
     uint4 v[8];
     load_eight(c, 0, v);
-    const double s = chunk_squares(c, v, sum, wide, [] {});
+    double s = 0.0;
+    add_squares(s, c, v, sum, wide, [] {});
     if (threadIdx.x == 0)
       for (uint32_t r = 0; r < size; r++) row::st_remote(row::remote(&parts[i], r), __double_as_longlong(s));
   }
