@@ -350,6 +350,7 @@ __global__ __launch_bounds__(NT) void logprob_reread_kernel(const LogprobArgs a)
   __shared__ uint64_t box[kMaxCluster];
   __shared__ uint64_t part[NT / 32];
   const uint32_t size = cluster_size(), rank = cluster_rank();
+  cluster_begun();
   const int64_t row = blockIdx.x / size;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const T *p = static_cast<const T *>(a.logits) + row * a.stride;
@@ -370,6 +371,7 @@ __global__ __launch_bounds__(NT) void logprob_reread_kernel(const LogprobArgs a)
   __syncthreads();
   float m, s;
   join(part, NT / 32, m, s);
+  cluster_wait_begun();
   cluster_post(pair(m, s), box, rank, size);   // no CTA reads or writes another's memory after this
   join(box, (int32_t)size, m, s);
   const float base = m == -INFINITY ? 0.0f : m;

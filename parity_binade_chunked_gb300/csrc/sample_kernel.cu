@@ -244,6 +244,7 @@ template <typename T, int NT>
 __global__ __launch_bounds__(NT) void sample_reread_kernel(const SampleArgs a) {
   __shared__ Shared sh;
   const uint32_t size = cluster_size(), rank = cluster_rank();
+  cluster_begun();
   const int64_t row = blockIdx.x / size;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Sampler<T, NT> s(sh);
@@ -267,6 +268,7 @@ __global__ __launch_bounds__(NT) void sample_reread_kernel(const SampleArgs a) {
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < NT / 32; i++) m = fmaxf(m, __uint_as_float((uint32_t)sh.warp[i]));
+  cluster_wait_begun();
   cluster_post(__float_as_uint(m), sh.box[0], rank, size);
   for (uint32_t r = 0; r < size; r++) m = fmaxf(m, __uint_as_float((uint32_t)sh.box[0][r]));
 

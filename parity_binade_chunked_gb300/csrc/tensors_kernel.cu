@@ -367,24 +367,28 @@ __global__ __launch_bounds__(kThreads, 1) void short_kernel(const TensorsArgs a)
   BlockSum<float> sum{table};
   BlockSum<double> wide{wide_table};
   const uint32_t size = row::cluster_size(), rank = row::cluster_rank();
-  for (int i = rank; i < a.nchunks; i += size) {
-    const Chunk c = a.chunks[i];
+  row::cluster_begun();
+  const bool any = (int)rank < a.nchunks;   // a chunk a CTA
+  Chunk c = {};
+  double s = 0.0;
+  if (any) {
+    c = a.chunks[rank];
     uint4 v[8];
     load_eight(c, 0, v);
-    double s = 0.0;
     add_squares(s, c, v, sum, wide, [] {});
-    if (threadIdx.x == 0)
-      for (uint32_t r = 0; r < size; r++) row::st_remote(row::remote(&parts[i], r), __double_as_longlong(s));
   }
+  row::cluster_wait_begun();
+  if (any && threadIdx.x == 0)
+    for (uint32_t r = 0; r < size; r++) row::st_remote(row::remote(&parts[rank], r), __double_as_longlong(s));
   row::cluster_sync();
-  double s = 0.0;
+  s = 0.0;
   if ((int)(threadIdx.x & 31) < a.nchunks) s = __longlong_as_double(parts[threadIdx.x & 31]);
   s = warp_add(s);
   const float norm = norm_of(a, s);
   if (rank == 0 && threadIdx.x == 0) *a.norm = norm;
   if (kClip) {
     const float f = factor_of(a, norm);
-    for (int i = rank; i < a.nchunks; i += size) scale_chunk(a.chunks[i], f);
+    if (any) scale_chunk(c, f);
   }
 }
 
