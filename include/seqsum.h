@@ -176,7 +176,9 @@ int seqsum_f64_planned(seqsum_plan *plan, const double *x, int64_t n, double s0,
  * of the sums above: their bits are defined.  The calls below enqueue on
  * `stream` and return without waiting, allocate nothing (seqsum_tensors_create
  * apart), use no workspace of a stream and may be captured into graphs.
- * seqsum_get_stats() does not cover them. */
+ * seqsum_get_stats() does not cover them.  Their kernels' waits are bounded
+ * too (2 s, whatever seqsum_debug_set_fault says); one that gave up shows in
+ * the results alone: token -1 with a logp of NaN, or NaN. */
 
 enum { SEQSUM_FP32 = 0, SEQSUM_FP16 = 1, SEQSUM_BF16 = 2 };
 
@@ -359,7 +361,8 @@ int seqsum_debug_counters(unsigned long long *out, int n);
 /* Test hook for the bounded waits: mode 1 withholds the header of tile `arg`
  * in later calls (the walk's wait for it must give up, write NaN and report
  * SEQSUM_ETIMEOUT, site 3); mode 0 restores normal calls.  wait_ns > 0 sets
- * the limit of every bounded device wait of later calls (0: the default, 2 s).
+ * the limit of every bounded device wait of later calls of the sequential sums
+ * (0: the default, 2 s).
  * Returns SEQSUM_OK or SEQSUM_EINVAL. */
 int seqsum_debug_set_fault(int mode, int64_t arg, int64_t wait_ns);
 
