@@ -17,7 +17,7 @@ import sys
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 
-def train(steps=60, seed=0, states=16, hidden=64, vocab=101, batch=512, max_norm=0.5, rate=2.0):
+def train(steps=60, seed=0, states=16, hidden=64, vocab=101, batch=512, max_norm=0.03, rate=2.0):
     """Returns the mean reward of each step (a list) and the norms before clipping."""
     import torch
 
