@@ -1,10 +1,12 @@
 """TensorList: the norm of many tensors and clipping by it, against 64 bits.
 
-Tolerance of the norm: a chunk's fp32 sum goes through at most 16 additions of
-a chain and 11 of trees, each rounding a sum of non-negative numbers, so it is
-off by at most 27 * 2^-24 of itself; the square root halves that, the result
-rounds once: REL = 8.7e-7.  A clipped number: that, four roundings of the
-factor and the product, and the rounding to its type."""
+Tolerance of the norm: a 16-bit chunk's fp32 sum goes through at most 16
+additions of a chain and 11 of trees, each rounding a sum of non-negative
+numbers, so it is off by at most 27 * 2^-24 of itself; the square root halves
+that, the result rounds once: REL = 8.7e-7.  (An fp32 chunk's chains are 32
+long, which bounds it by 42 * 2^-24; the tolerance for it is the same, tighter
+one: roundings of both signs do not reach either.)  A clipped number: that, four
+roundings of the factor and the product, and the rounding to its type."""
 import math
 
 import numpy as np
