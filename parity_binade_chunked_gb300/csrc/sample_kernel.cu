@@ -400,13 +400,13 @@ constexpr int kMost = is_far(K) ? 1 : kMaxCluster;   // CTAs a row at most
 // without top-k and top-p have no use for lists; they get a third buffer.
 template <int W, Kind K>
 struct Picks {
-  static constexpr int kBinsHere = searches(K) ? kBins : 1, kListHere = searches(K) ? kList : 1,
-                       kOwnHere = searches(K) ? kOwn<K> : 1, kBoxes = kMost<K> * W;
+  static constexpr int kBinsHere = searches(K) ? kBins : 1, kPartHere = K == kSearch ? kBins : 1,
+                       kListHere = searches(K) ? kList : 1, kOwnHere = searches(K) ? kOwn<K> : 1, kBoxes = kMost<K> * W;
   uint64_t full[3], empty[3], told[4], parts, totals, entries;
   uint64_t box[4][kBoxes];        // a word of every warp of the cluster
   uint64_t step_mass[is_far(K) ? kFarSteps / W : 32];   // of the segment that the token is in
   uint4 bins[kBinsHere];          // a split of the CTA's entries: count, and mass in three parts
-  uint4 part[kBinsHere];          // this CTA's share of the bins, of every CTA
+  uint64_t part[2][kPartHere];    // this CTA's share of the bins, of every CTA: count and mass; rounds take turns
   uint4 total[kBinsHere];         // the bins summed over the cluster: count, mass
   uint32_t listed, small_listed;
   uint4 small[32];                // the last few entries of a search: key, index, weight
@@ -493,6 +493,13 @@ struct Picker {
   // of each: every CTA sums its share of the bins and sends the sums around.
   // (Sent with asynchronous stores: a release of plain ones to the cluster
   // took 1300 to 5000 cycles, reading 256 bins of 8 CTAs 2000.)
+  // What says that no one still reads what is written here: another CTA has
+  // its sums, and so goes on, once those of this CTA's threads that sum for it
+  // have sent theirs; the threads that sum for others may still be reading
+  // `part`.  So rounds take two of them in turn: a round's words come after the
+  // sums of the round before, which come after all of this CTA's warps began
+  // that round, so after their reads two rounds back.  `total` needs one: its
+  // words come after the sender had this CTA's words of the same round.
   __device__ __forceinline__ void total_bins() {
     team();
     if (is_far(K) || size == 1) {
@@ -505,21 +512,22 @@ struct Picker {
       return;
     }
     const uint32_t share = kBins / size, to = threadIdx.x / share, bin = threadIdx.x % share, parity = totalled++ & 1;
+    uint64_t *part = sh.part[parity];
     if (threadIdx.x < kBins) {
       const uint4 v = sh.bins[threadIdx.x];
       const uint64_t w = mass_of(v);
-      send(&sh.part[rank * share + bin], &sh.parts, to, make_uint4(v.x, (uint32_t)w, (uint32_t)(w >> 32), 0));
+      send(reinterpret_cast<uint2 *>(&part[rank * share + bin]), &sh.parts, to, make_uint2((uint32_t)w, (uint32_t)(w >> 32) | v.x << 16));
     }
     came &= bar_wait(&sh.parts, parity);
-    if (threadIdx.x == 0) bar_expect(&sh.parts, kBins * 16);
+    if (threadIdx.x == 0) bar_expect(&sh.parts, kBins * 8);
     if (threadIdx.x < kBins) {
       uint32_t n = 0;
       uint64_t w = 0;
 #pragma unroll
       for (uint32_t c = 0; c < kMaxCluster; c++)
         if (c < size) {
-          const uint4 v = sh.part[c * share + bin];
-          n += v.x, w += v.y + ((uint64_t)v.z << 32);
+          const uint64_t v = part[c * share + bin];   // a slice's count fits 16 bits, its mass 48
+          n += (uint32_t)(v >> 48), w += v & ((1ull << 48) - 1);
         }
       send(&sh.total[rank * share + bin], &sh.totals, to, make_uint4(n, (uint32_t)w, (uint32_t)(w >> 32), 0));
     }
@@ -1058,7 +1066,7 @@ __global__ __launch_bounds__(W * 32, W == 8 || K == kFarSearch || (K == kFarPlai
       bar_init(&sh.told[b], 1);
       bar_expect(&sh.told[b], size * W * 8);
     }
-    bar_init(&sh.parts, 1), bar_expect(&sh.parts, kBins * 16);
+    bar_init(&sh.parts, 1), bar_expect(&sh.parts, kBins * 8);
     bar_init(&sh.totals, 1), bar_expect(&sh.totals, kBins * 16);
     bar_init(&sh.entries, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -1324,6 +1332,9 @@ constexpr int kDevices = 16;   // whose occupancy is kept (for a function, a num
 
 template <int W, Kind K>
 constexpr int kMostSteps = is_far(K) ? 1 : (int)(((226 << 10) - sizeof(Picks<W, K>)) / ((kBuffers<K> + (is_far(K))) * 32 * 16));
+
+static_assert(kMostSteps<8, kSearch> * 32 * 8 < 1 << 16 && kMostSteps<16, kSearch> * 32 * 8 < 1 << 16,
+              "the entries of a CTA's slice are counted in 16 bits, their mass of 2^31 each in 48");
 
 template <typename T, int W, Kind K>
 int run_sample(SampleArgs a, int size, int log2, cudaStream_t stream) {
