@@ -995,8 +995,7 @@ struct Picker {
               continue;
             }
           }
-          from = fmaxf(-e1 * 0.125f, kFloor + 1e-5f);
-          if (how == kCount && e1 == kBins) from = kFloor;
+          from = fmaxf(-e1 * 0.125f, kFloor);   // what is counted is what list() lists: all above kFloor in the last eighth
           sampled = how == kSample;
           if (!by_k) collect(from);
         }
