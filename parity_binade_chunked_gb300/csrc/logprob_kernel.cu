@@ -34,6 +34,7 @@ struct LogprobArgs {
   int64_t dstride;
   int32_t parts;                                     // backward: CTAs a row
   int32_t steps;                                     // that a CTA takes of a row at most
+  Waits waits;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -140,6 +141,13 @@ __device__ __forceinline__ void write_zeros(const S &x, T *d, bool aligned) {
   for (int k = 0; k < x.steps; k++) x.write(d, aligned, k, y);
 }
 
+// NaN to elements [from, to) of a row, by one warp
+template <typename T>
+__device__ __noinline__ void write_nan(T *d, int32_t from, int32_t to) {
+#pragma unroll 1
+  for (int32_t i = from + (int32_t)(threadIdx.x & 31); i < to; i += 32) Elem<T>::store(d + i, NAN);
+}
+
 template <typename T>
 __device__ __forceinline__ bool same_alignment(const T *d, int32_t off) {
   return (reinterpret_cast<uintptr_t>(d) & 15) / sizeof(T) == (uintptr_t)off;
@@ -163,6 +171,9 @@ constexpr int kLag = kGrad ? 0 : 1;
 // than room for them.  Bound by HBM with gradient: 8192 x 131072 bf16 695 us
 // (6.2 of 6.8 TB/s), 4000 x 50000 133 us (6.0).  Without: 4096 x 50001 70 us
 // (5.9 TB/s), 4096 x 131072 200 us (5.4), where issue slots are two thirds full.
+// A wait that gave up makes its row's sum NaN in every CTA (a word of NaN), or
+// in the warp that missed the words; what the warp has yet to write is marked
+// NaN after that, each place by the thread that would have written it.
 template <typename T, bool kGrad>
 __global__ __launch_bounds__(kWarps * 32 + 32) void logprob_kernel(const LogprobArgs a) {
   extern __shared__ uint4 buffers[];   // kB buffers of a.steps steps
@@ -191,20 +202,27 @@ __global__ __launch_bounds__(kWarps * 32 + 32) void logprob_kernel(const Logprob
   };
   bool ok = true;
   if (warp == kWarps) {
-    for (uint32_t it = 0, b = 0, use = 0; it < turns; it++) {
-      if (use > 0) ok = __all_sync(~0u, bar_wait(&empty[b], (use - 1) & 1));
+    uint32_t it = 0;
+    for (uint32_t b = 0, use = 0; it < turns; it++) {
+      if (use > 0) ok = __all_sync(~0u, bar_wait(&empty[b], (use - 1) & 1, a.waits.limit));
       if (!ok) break;
       stream(it, b).bring(static_cast<const T *>(a.logits) + row_of(it) * a.stride, &full[b]);
       if (++b == kB) b = 0, use++;
     }
+    // copies in flight land before the CTA goes
+    for (uint32_t i = it > kB ? it - kB : 0; i < it; i++) bar_wait(&full[i % kB], i / kB & 1);
   } else {
     const uint32_t segment = rank * kWarps + warp;
+    // the thread that has vector `vec` of the slice, and the token's vector
+    auto has = [&](int32_t vec) { return (int)threadIdx.x == vec % (kWarps * 32); };
+    auto vec_of = [&](const Stream<T> &x, int64_t token) { return (int32_t)(token + x.off) / kE - x.begin; };
     Stream<T> was;
     int64_t was_token = 0;
     float was_xt = 0.0f, was_dlogp = 0.0f;   // the logit of the token, in the thread that has it
     bool was_mine = false;
     uint32_t was_b = 0;
-    for (uint32_t it = 0, b = 0, parity = 0; it < turns + kL && ok; it++) {
+    uint32_t it = 0;
+    for (uint32_t b = 0, parity = 0; it < turns + kL && ok; it++) {
       Stream<T> x;
       int64_t token = 0;
       float xt = 0.0f, dlogp = 0.0f;
@@ -213,7 +231,7 @@ __global__ __launch_bounds__(kWarps * 32 + 32) void logprob_kernel(const Logprob
         x = stream(it, b);
         token = a.tokens[row_of(it)];
         if (kGrad) dlogp = a.dlogps[row_of(it)];
-        ok &= bar_wait(&full[b], parity);
+        ok &= bar_wait(&full[b], parity, a.waits.limit) & !a.waits.fails(it, segment);
         const Exchange tell = {box[it % kBoxes], &told[it % kBoxes]};
         int32_t st = x.step_of(segment, log2_segments) - x.begin / 32;
         const int32_t end = x.step_of(segment + 1, log2_segments) - x.begin / 32;
@@ -229,27 +247,28 @@ __global__ __launch_bounds__(kWarps * 32 + 32) void logprob_kernel(const Logprob
           st += 2, p += 64;
         }
         if (st < end) part.add<T, 1>(p);
+        if (!ok) part.s = NAN;   // the wait gave up: so is the row's sum, in every CTA
         tell.post(segment, part.of_warp(), size);
-        const int32_t vec = (int32_t)(token + x.off) / kE - x.begin;   // the token's
-        if (token >= 0 && token < a.vocab && vec >= 0 && vec < x.n && (int)threadIdx.x == vec % (kWarps * 32)) {
+        const int32_t vec = vec_of(x, token);
+        if (token >= 0 && token < a.vocab && vec >= 0 && vec < x.n && has(vec)) {
           xt = Elem<T>::load(reinterpret_cast<const T *>(x.buf + vec) + (token - x.index(vec, 0)));
           have = true;
         }
         if (!kGrad) {
           __syncwarp();
-          if (lane == 0) bar_arrive(&empty[b]);
+          if (ok && lane == 0) bar_arrive(&empty[b]);
         }
       }
       if (!kL) was = x, was_token = token, was_xt = xt, was_dlogp = dlogp, was_mine = have, was_b = b;
       if (it >= kL) {
         const int64_t row = row_of(it - kL);
         const uint32_t t = (it - kL) % kBoxes;
-        ok &= bar_wait(&told[t], ((it - kL) / kBoxes) & 1);
-        if (threadIdx.x == 0) bar_expect(&told[t], segments * 8);   // for its next row
+        ok &= bar_wait(&told[t], ((it - kL) / kBoxes) & 1, a.waits.limit);
+        if (ok && threadIdx.x == 0) bar_expect(&told[t], segments * 8);   // for its next row
         float m, s;
         join(box[t], segments, m, s);
+        if (!__all_sync(~0u, ok)) s = NAN;
         const float base = m == -INFINITY ? 0.0f : m;
-        if (!__all_sync(~0u, ok)) s = NAN;   // a wait gave up
         const bool used = was_token >= 0 && was_token < a.vocab, nothing = s == 0.0f;
         if (rank == 0 && threadIdx.x == 0) {
           a.lses[row] = base + logf(s);
@@ -278,22 +297,33 @@ __global__ __launch_bounds__(kWarps * 32 + 32) void logprob_kernel(const Logprob
             else was.write_edge(d, vec, y);
           }
           __syncwarp();
-          if (lane == 0) bar_arrive(&empty[was_b]);
+          if (ok && lane == 0) bar_arrive(&empty[was_b]);
         }
       }
       if (kL) was = x, was_token = token, was_xt = xt, was_dlogp = dlogp, was_mine = have, was_b = b;
       if (++b == kB) b = 0, parity ^= 1;
       ok = __all_sync(~0u, ok);
-      if (!ok && rank == 0 && lane == 0)   // what is not done is marked
-        for (uint32_t i = it >= kL ? it - kL : 0; i < turns; i++) a.lses[row_of(i)] = a.logps[row_of(i)] = NAN;
     }
-    // copies in flight land before the CTA goes (in a call that went well none are)
-    if (!ok)
-      for (int b = 0; b < kB; b++)
-        for (uint32_t parity = 0; parity < 2; parity++) bar_wait(&full[b], parity);
+    if (!ok) {
+      // what this warp has yet to write is marked, each place by the thread that would have written it
+      for (uint32_t i = it > kL ? it - kL : 0; i < turns; i++) {
+        const int64_t row = row_of(i), token = a.tokens[row];
+        const Stream<T> x = stream(i, 0);
+        const bool used = token >= 0 && token < a.vocab;
+        const int32_t vec = vec_of(x, token);
+        if (rank == 0 && threadIdx.x == 0) a.lses[row] = NAN;
+        if (used ? vec >= 0 && vec < x.n && has(vec) : rank == 0 && threadIdx.x == 0) a.logps[row] = NAN;
+        if constexpr (kGrad) {
+          const int32_t from = x.index((x.step_of(segment, log2_segments) - x.begin / 32) * 32, 0),
+                        to = x.index((x.step_of(segment + 1, log2_segments) - x.begin / 32) * 32, 0);
+          write_nan(static_cast<T *>(a.dlogits) + row * a.dstride, max(from, 0), min(to, a.vocab));
+        }
+      }
+    }
   }
   __syncwarp();
   cluster_sync();
+  if (!ok) stay();
 }
 
 // Short rows: a warp each, in registers; no barrier, no exchange.  (8192 x 3001 bf16 rows, gradient:
@@ -502,7 +532,7 @@ int seqsum_token_logprob(const void *logits, int32_t dtype, int64_t rows, int64_
   if (sq::bad_rows(logits, dtype, rows, vocab, row_stride)) return SEQSUM_EINVAL;
   if (rows == 0) return SEQSUM_OK;
   if (!tokens || !logps || !lses) return SEQSUM_EINVAL;
-  sq::LogprobArgs a = {logits, rows, row_stride, (int32_t)vocab, tokens, logps, lses, nullptr, nullptr, nullptr, 0, 1, 0};
+  sq::LogprobArgs a = {logits, rows, row_stride, (int32_t)vocab, tokens, logps, lses, nullptr, nullptr, nullptr, 0, 1, 0, sq::row::waits()};
   if (dtype == SEQSUM_FP32) return sq::choose_logprob<float, false>(a, stream);
   if (dtype == SEQSUM_FP16) return sq::choose_logprob<__half, false>(a, stream);
   return sq::choose_logprob<__nv_bfloat16, false>(a, stream);
@@ -515,7 +545,7 @@ int seqsum_token_logprob_grad(const void *logits, int32_t dtype, int64_t rows, i
     return SEQSUM_EINVAL;
   if (rows == 0) return SEQSUM_OK;
   if (!tokens || !dlogps || !logps || !lses || (rows > 1 && drow_stride < vocab)) return SEQSUM_EINVAL;
-  sq::LogprobArgs a = {logits, rows, row_stride, (int32_t)vocab, tokens, logps, lses, dlogps, nullptr, dlogits, drow_stride, 1, 0};
+  sq::LogprobArgs a = {logits, rows, row_stride, (int32_t)vocab, tokens, logps, lses, dlogps, nullptr, dlogits, drow_stride, 1, 0, sq::row::waits()};
   if (dtype == SEQSUM_FP32) return sq::choose_logprob<float, true>(a, stream);
   if (dtype == SEQSUM_FP16) return sq::choose_logprob<__half, true>(a, stream);
   return sq::choose_logprob<__nv_bfloat16, true>(a, stream);
@@ -528,7 +558,7 @@ int seqsum_token_logprob_backward(const void *logits, int32_t dtype, int64_t row
     return SEQSUM_EINVAL;
   if (rows == 0 || vocab == 0) return SEQSUM_OK;
   if (!tokens || !dlogps || !lses || (rows > 1 && drow_stride < vocab)) return SEQSUM_EINVAL;
-  sq::LogprobArgs a = {logits, rows, row_stride, (int32_t)vocab, tokens, nullptr, nullptr, dlogps, lses, dlogits, drow_stride, 1, 0};
+  sq::LogprobArgs a = {logits, rows, row_stride, (int32_t)vocab, tokens, nullptr, nullptr, dlogps, lses, dlogits, drow_stride, 1, 0, sq::row::waits()};
   if (dtype == SEQSUM_FP32) return sq::run_backward<float>(a, stream);
   if (dtype == SEQSUM_FP16) return sq::run_backward<__half>(a, stream);
   return sq::run_backward<__nv_bfloat16>(a, stream);

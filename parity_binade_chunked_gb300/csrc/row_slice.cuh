@@ -18,6 +18,10 @@ int multiprocessors();
 
 namespace row {
 
+struct Waits;
+// What the next call's waits are given (seqsum_debug_set_fault).
+Waits waits();
+
 constexpr int kMaxCluster = 8;           // the portable cluster size
 constexpr int64_t kMaxVocab = 1 << 24;   // element indices fit 32 bits, 2^24 weights of 2^31 fit 64
 
@@ -338,7 +342,20 @@ struct Slice {
 // after every warp has left the exchange three before, so there are four boxes
 // in turn.
 
-constexpr uint64_t kWaitNs = 2000000000ull;   // waits for copies and for other CTAs give up after 2 s
+// Waits for copies and for other CTAs are bounded.  A warp whose wait gave up
+// has nothing computed from what it did not have: the word that it owes says
+// so, or is not sent; later ones are not, so that the others' waits run out too;
+// and each marks what it had yet to write.
+
+constexpr uint32_t kWaitNs = 2000000000u;   // the limit of a wait
+
+// A call's limit, and, for tests, a wait that is taken to have given up: that
+// of warp `warp` of each cluster for its row `turn` (-1: none).
+struct Waits {
+  uint32_t limit;
+  int32_t turn, warp;
+  __device__ __forceinline__ bool fails(uint32_t it, uint32_t of) const { return it == (uint32_t)turn && of == (uint32_t)warp; }
+};
 
 __device__ __forceinline__ uint32_t smem(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void bar_init(uint64_t *bar, uint32_t count) {
@@ -360,19 +377,28 @@ __device__ __forceinline__ bool bar_try(uint64_t *bar, uint32_t parity) {
       : "memory");
   return done;
 }
-static __device__ __noinline__ bool bar_wait_long(uint64_t *bar, uint32_t parity) {
+static __device__ __noinline__ bool bar_wait_long(uint64_t *bar, uint32_t parity, uint32_t limit) {
   uint64_t t0, t;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
   do {
     for (int i = 0; i < 64; i++)
       if (bar_try(bar, parity)) return true;
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  } while (t - t0 < kWaitNs);
+  } while (t - t0 < limit);
   return false;
 }
-// false: gave up
-__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity) {
-  return bar_try(bar, parity) || bar_wait_long(bar, parity);
+// false: gave up (of a warp's lanes, some may have)
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, uint32_t limit = kWaitNs) {
+  return bar_try(bar, parity) || bar_wait_long(bar, parity, limit);
+}
+// A CTA whose waits gave up stays a millisecond past the cluster's last barrier:
+// words that others had sent it by then, and that it did not wait for, land in
+// its memory.
+static __device__ __noinline__ void stay() {
+  uint64_t t0, t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+  do asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  while (t - t0 < 1000000);
 }
 
 // 16 bytes to shared memory of CTA `rank`, counted down at its `bar`.

@@ -56,6 +56,8 @@ int g_plan_mode = 0;
 int g_fault_mode = 0;
 int64_t g_fault_arg = 0;
 uint64_t g_wait_ns = 2000000000ull;   // every bounded device wait gives up after 2 s
+std::atomic<uint32_t> g_row_wait_ns{sq::row::kWaitNs};   // the same for the kernels on rows of logits
+std::atomic<int32_t> g_row_turn{-1}, g_row_warp{0};
 int g_blocks_per_sm = 0;
 int64_t g_wave = 0;                   // plan units run this many tiles ahead of run units (0: not yet read)
 int g_num_sms[64] = {0};
@@ -267,6 +269,11 @@ namespace sq {
 
 // for the other translation units' entries (row_slice.cuh)
 int note_cuda(cudaError_t e) { return cuda_fail(e); }
+
+row::Waits row::waits() {
+  return {g_row_wait_ns.load(std::memory_order_relaxed), g_row_turn.load(std::memory_order_relaxed),
+          g_row_warp.load(std::memory_order_relaxed)};
+}
 
 int multiprocessors() {
   static std::atomic<int> known[64];
@@ -610,10 +617,13 @@ int seqsum_debug_set_plan(int mode) {
 
 int seqsum_debug_set_fault(int mode, int64_t arg, int64_t wait_ns) {
   std::lock_guard<std::mutex> lk(g_mu);
-  if (mode < 0 || mode > 1 || wait_ns < 0) return SEQSUM_EINVAL;
-  g_fault_mode = mode;
+  if (mode < 0 || mode > 2 || wait_ns < 0 || (mode == 2 && (arg < 0 || arg >= (int64_t)1 << 34))) return SEQSUM_EINVAL;
+  g_fault_mode = mode == 1 ? 1 : 0;
   g_fault_arg = arg;
   g_wait_ns = wait_ns > 0 ? (uint64_t)wait_ns : 2000000000ull;
+  g_row_turn = mode == 2 ? (int32_t)(arg >> 7) : -1;
+  g_row_warp = (int32_t)(arg & 127);
+  g_row_wait_ns = wait_ns == 0 ? sq::row::kWaitNs : wait_ns < 0xffffffffll ? (uint32_t)wait_ns : 0xffffffffu;
   return SEQSUM_OK;
 }
 
