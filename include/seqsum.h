@@ -179,7 +179,7 @@ int seqsum_f64_planned(seqsum_plan *plan, const double *x, int64_t n, double s0,
  * seqsum_get_stats() does not cover them.  Their kernels' waits are bounded
  * too (2 s; seqsum_debug_set_fault); one that gave up shows in the results
  * alone: NaN in what was not computed (a row's lse, logp, its gradient or a
- * part of that), and token -1 with a logp of NaN. */
+ * part of that), and a token of -1 or a logp of NaN from sampling. */
 
 enum { SEQSUM_FP32 = 0, SEQSUM_FP16 = 1, SEQSUM_BF16 = 2 };
 
@@ -363,10 +363,10 @@ int seqsum_debug_counters(unsigned long long *out, int n);
  * in later calls (the walk's wait for it must give up, write NaN and report
  * SEQSUM_ETIMEOUT, site 3); mode 0 restores normal calls.  wait_ns > 0 sets
  * the limit of every bounded device wait of later calls of the sequential sums
- * and of seqsum_token_logprob and _grad (0: the default, 2 s).  Mode 2: in later
- * calls of these two on rows that are streamed through shared memory, warp
- * arg % 128 of each cluster takes its wait for the cluster's row number
- * arg / 128 as given up.
+ * and of the kernels on rows of logits (0: the default, 2 s).  Mode 2: in later
+ * calls of seqsum_sample_tokens, seqsum_token_logprob and _grad, where they
+ * stream rows through shared memory, warp arg % 128 of each cluster takes its
+ * wait for the cluster's row number arg / 128 as given up.
  * Returns SEQSUM_OK or SEQSUM_EINVAL. */
 int seqsum_debug_set_fault(int mode, int64_t arg, int64_t wait_ns);
 

@@ -53,6 +53,7 @@ struct SampleArgs {
   int64_t *tokens;
   float *logps;
   int32_t steps;   // that a CTA takes of a row at most
+  Waits waits;
 };
 
 // A place in the order: an entry is before it where its key (the bits of -d)
@@ -377,7 +378,6 @@ __global__ __launch_bounds__(NT) void sample_reread_kernel(const SampleArgs a) {
 // A row has three parts: its maximum; what is kept of it and the mass of that
 // by segments; the place of the token.  The words of a part travel while the
 // next row's first part is worked on.
-
 //
 // Where the rows are many, a CTA takes a row to itself: it reads the row from
 // HBM once and from L2 in the later passes, and tells no one anything.  Twice
@@ -403,6 +403,7 @@ struct Picks {
   static constexpr int kBinsHere = searches(K) ? kBins : 1, kPartHere = K == kSearch ? kBins : 1,
                        kListHere = searches(K) ? kList : 1, kOwnHere = searches(K) ? kOwn<K> : 1, kBoxes = kMost<K> * W;
   uint64_t full[3], empty[3], told[4], parts, totals, entries;
+  uint32_t begun, whole;          // rows whose copy is on its way, whose edges are too (for the warp that brings them)
   uint64_t box[4][kBoxes];        // a word of every warp of the cluster
   uint64_t step_mass[is_far(K) ? kFarSteps / W : 32];   // of the segment that the token is in
   uint4 bins[kBinsHere];          // a split of the CTA's entries: count, and mass in three parts
@@ -435,6 +436,7 @@ struct Picker {
   int32_t st0, st1;     // this warp's steps
   float m, c;
   bool special;         // (v - m) * c needs care
+  uint32_t limit;       // of a wait
   bool came = true;     // no wait of this warp gave up
   bool ok = true;       // ... none of the CTA's, as of the last agreement
   int own = -1;         // entries that this warp took out of its segment, from own_from octaves on
@@ -446,7 +448,13 @@ struct Picker {
   // ---- the CTA's working warps, and the cluster's
 
   __device__ __forceinline__ void team() const { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kThreads) : "memory"); }
-  // all of the CTA's working warps go on together or give up together
+  // Once a wait gave up the warp waits no more and tells no one anything, so
+  // that no CTA goes on with what it did not have.
+  __device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity) {
+    came = came && __all_sync(~0u, bar_wait(bar, parity, limit));
+  }
+  // All of the CTA's working warps go on together or give up together: after
+  // every wait for another CTA, before a warp takes its way by what came.
   __device__ __forceinline__ void agree() {
     if (is_far(K)) return;   // (no waits that could give up)
     uint32_t all;
@@ -468,14 +476,14 @@ struct Picker {
     }
     const Exchange e = {sh.box[posted & 3], &sh.told[posted & 3]};
     posted++;
-    e.post((int32_t)(rank * W + (threadIdx.x >> 5)), v, size);
+    if (came) e.post((int32_t)(rank * W + (threadIdx.x >> 5)), v, size);
   }
   __device__ __forceinline__ const uint64_t *hear() {
     const uint32_t b = heard & 3, parity = (heard >> 2) & 1;
     heard++;
     if (is_far(K)) return team(), sh.box[b];
-    came &= bar_wait(&sh.told[b], parity);
-    if (threadIdx.x == 0) bar_expect(&sh.told[b], size * W * 8);
+    wait(&sh.told[b], parity);
+    if (came && threadIdx.x == 0) bar_expect(&sh.told[b], size * W * 8);
     return sh.box[b];
   }
   // The sum of the words heard.
@@ -500,7 +508,9 @@ struct Picker {
   // sums of the round before, which come after all of this CTA's warps began
   // that round, so after their reads two rounds back.  `total` needs one: its
   // words come after the sender had this CTA's words of the same round.
-  __device__ __forceinline__ void total_bins() {
+  // Returns the words posted before it, where there are some to hear.
+  __device__ __forceinline__ const uint64_t *total_bins(bool posted_words) {
+    const uint64_t *box = nullptr;
     team();
     if (is_far(K) || size == 1) {
       if (threadIdx.x < kBins) {
@@ -508,19 +518,21 @@ struct Picker {
         const uint64_t w = mass_of(v);
         sh.total[threadIdx.x] = make_uint4(v.x, (uint32_t)w, (uint32_t)(w >> 32), 0);
       }
-      team();
-      return;
+      if (posted_words) box = hear();
+      if (!is_far(K)) agree();
+      else if (!posted_words) team();
+      return box;
     }
     const uint32_t share = kBins / size, to = threadIdx.x / share, bin = threadIdx.x % share, parity = totalled++ & 1;
     uint64_t *part = sh.part[parity];
-    if (threadIdx.x < kBins) {
+    if (came && threadIdx.x < kBins) {
       const uint4 v = sh.bins[threadIdx.x];
       const uint64_t w = mass_of(v);
       send(reinterpret_cast<uint2 *>(&part[rank * share + bin]), &sh.parts, to, make_uint2((uint32_t)w, (uint32_t)(w >> 32) | v.x << 16));
     }
-    came &= bar_wait(&sh.parts, parity);
-    if (threadIdx.x == 0) bar_expect(&sh.parts, kBins * 8);
-    if (threadIdx.x < kBins) {
+    wait(&sh.parts, parity);
+    if (came && threadIdx.x == 0) bar_expect(&sh.parts, kBins * 8);
+    if (came && threadIdx.x < kBins) {
       uint32_t n = 0;
       uint64_t w = 0;
 #pragma unroll
@@ -531,9 +543,11 @@ struct Picker {
         }
       send(&sh.total[rank * share + bin], &sh.totals, to, make_uint4(n, (uint32_t)w, (uint32_t)(w >> 32), 0));
     }
-    came &= bar_wait(&sh.totals, parity);
-    if (threadIdx.x == 0) bar_expect(&sh.totals, kBins * 16);
+    wait(&sh.totals, parity);
+    if (came && threadIdx.x == 0) bar_expect(&sh.totals, kBins * 16);
+    if (posted_words) box = hear();
     agree();
+    return box;
   }
   __device__ __forceinline__ void clear_bins() {
     if (threadIdx.x < kBins) sh.bins[threadIdx.x] = make_uint4(0, 0, 0, 0);
@@ -714,6 +728,8 @@ struct Picker {
     }
   };
 
+  // (What find, sample and count return means nothing where the CTA gave up in them.)
+
   // Splits the entries of `r` and finds the first bin at which their count (or
   // mass) reaches `need`.  Over the row, entries from `from` octaves on are
   // looked at, and the mass of those before `r` comes before all bins.
@@ -730,8 +746,8 @@ struct Picker {
       const float lo = __uint_as_float(r.lo);
       if (r.scale > 0.0f) post(r.lo > 0 ? row_sum(from, [&](float d, int32_t) { return -d < lo ? weight(d) : 0; }) : 0);
       row_entries(from, -lo, take);
-      total_bins();
-      front = r.scale > 0.0f ? sum_of(hear()) : 0;
+      const uint64_t *box = total_bins(r.scale > 0.0f);
+      front = r.scale > 0.0f ? sum_of(box) : 0;
     } else {
       list_entries(take);
       team();
@@ -847,7 +863,7 @@ struct Picker {
     const uint32_t at = __shfl_sync(~0u, ends - theirs, rank);
     for (uint32_t i = threadIdx.x; i < mine * size; i += kThreads) send(&sh.all[at + i / size], &sh.entries, i % size, sh.list[i / size]);
     if (threadIdx.x == 0) bar_expect(&sh.entries, total * 8);
-    came &= bar_wait(&sh.entries, shared_lists++ & 1);
+    wait(&sh.entries, shared_lists++ & 1);
     agree();
     listed = (int32_t)total;
   }
@@ -871,8 +887,8 @@ struct Picker {
       if (d[0] > kFloor) atomicAdd(&sh.bins[(int)(-d[0] * 8.0f)].x, 1u);
     });
     post(warp_sum(mine));
-    total_bins();
-    const uint64_t all = max((uint64_t)1, sum_of(hear())), cut = max((uint64_t)1, share(part_of(top_p), all));
+    const uint64_t *box = total_bins(true);
+    const uint64_t all = max((uint64_t)1, sum_of(box)), cut = max((uint64_t)1, share(part_of(top_p), all));
     auto middle = [&](int i) { return ex2(30.9375f - (lane * kPer + i) * 0.125f) * kE; };
     float w[kPer], tail = 0.0f, tail2 = 0.0f;   // the tail's mass from an eighth on, and its variance
 #pragma unroll
@@ -917,8 +933,8 @@ struct Picker {
       mine += weight(d);
     });
     post(warp_sum(mine));
-    total_bins();
-    const uint64_t all = max((uint64_t)1, sum_of(hear())), cut = max((uint64_t)1, share(part_of(top_p), all));
+    const uint64_t *box = total_bins(true);
+    const uint64_t all = max((uint64_t)1, sum_of(box)), cut = max((uint64_t)1, share(part_of(top_p), all));
     uint32_t counts[kPer], n = 0;
 #pragma unroll
     for (int i = 0; i < kPer; i++) n += counts[i] = sh.total[lane * kPer + i].x;
@@ -930,7 +946,7 @@ struct Picker {
         const int o = __ffs(reached) - 1;
         uint32_t before = __shfl_sync(~0u, upto - n, o);
         e0 = o * kPer;
-        while (before + sh.total[e0].x < (uint32_t)top_k) before += sh.total[e0++].x;
+        while (ok && before + sh.total[e0].x < (uint32_t)top_k) before += sh.total[e0++].x;
         e1 = e0 + 1;
         return (uint32_t)top_k - before;
       }
@@ -986,8 +1002,10 @@ struct Picker {
         } else {
           if (how == kSample) {
             need = sample(top_p, e0, e1);
+            if (!ok) break;
           } else {
             need = count(by_k ? top_k : 0, least, top_p, e0, e1);
+            if (!ok) break;
             if (by_k && e1 == 0) {   // all that weighs anything is among the first k
               if (!by_p) break;
               by_k = false;
@@ -1020,6 +1038,7 @@ struct Picker {
         end = r.ties() ? Place{r.lo, r.ihi} : Place{r.hi, 0};
       } else {
         const Found f = find(!by_k, need, r, from);
+        if (!ok) break;
         if (f.bin < 0) {
           if (!sampled) return Place{r.hi, 0};   // (cannot be: what is not reached is less than all)
           how = kCount;                          // the sample misled
@@ -1084,7 +1103,7 @@ __global__ __launch_bounds__(W * 32, W == 8 || K == kFarSearch || (K == kFarPlai
   auto row_at = [&](uint32_t it) { return static_cast<const T *>(a.logits) + row_of(it) * a.stride; };
   {
     Picker<T, W, K> s(sh);
-    s.rank = rank, s.size = size;
+    s.rank = rank, s.size = size, s.limit = a.waits.limit;
     constexpr int kPer = (kMost<K> * W + 31) / 32;
     const uint32_t half = size * W / 2;
     const int log2_segments = log2_size + kLog2W;
@@ -1104,7 +1123,10 @@ __global__ __launch_bounds__(W * 32, W == 8 || K == kFarSearch || (K == kFarPlai
       place(it);
       const bool greedy = !(temperature_of(row_of(it)) > 0.0f);
       const int32_t top_k = top_k_of(row_of(it));
-      if (!is_far(K)) s.came &= bar_wait(&sh.full[it % kB], it / kB & 1);
+      if (!is_far(K)) {
+        s.wait(&sh.full[it % kB], it / kB & 1);
+        s.came = s.came && !a.waits.fails(it, rank * W + warp);
+      }
       float m = -INFINITY;
       s.steps([&](int32_t, uint4 v) { m = Elem<T>::vec_max(v, m); });
       const float of_thread = m;
@@ -1134,12 +1156,14 @@ __global__ __launch_bounds__(W * 32, W == 8 || K == kFarSearch || (K == kFarPlai
       s.post(((uint64_t)beside << 32) | __float_as_uint(m));
     };
 
-    if (!is_far(K) && warp == 0)
+    if (!is_far(K) && warp == 0) {
       for (uint32_t i = 0; i < kB && i < turns; i++) {
         const Stream<T> x = stream(i);
         x.bring_inner(row_at(i), &sh.full[i]);
         x.bring_edges(x.edge(row_at(i)), &sh.full[i]);
       }
+      if (lane == 0) sh.begun = sh.whole = min((uint32_t)kB, turns);
+    }
     look(0);
     uint32_t it = 0;
     for (; it < turns; it++) {
@@ -1148,12 +1172,13 @@ __global__ __launch_bounds__(W * 32, W == 8 || K == kFarSearch || (K == kFarPlai
       float edge = 0.0f;
       bool bring = !is_far(K) && warp == 0 && it > 0 && next < turns;
       if (bring) {
-        s.came &= bar_wait(&sh.empty[(it - 1) % kB], (it - 1) / kB & 1);
-        bring = __all_sync(~0u, s.came);   // (if not, the CTA's next agreement ends it)
+        s.wait(&sh.empty[(it - 1) % kB], (it - 1) / kB & 1);
+        bring = s.came;   // (if not, the CTA's next agreement ends it)
       }
       if (bring) {
         const Stream<T> x = stream(next);
         x.bring_inner(row_at(next), &sh.full[next % kB]);
+        if (lane == 0) sh.begun = next + 1;
         edge = x.edge(row_at(next));
       }
       // the second part: what is kept of the row, and its mass by warps
@@ -1188,14 +1213,14 @@ __global__ __launch_bounds__(W * 32, W == 8 || K == kFarSearch || (K == kFarPlai
       };
       const bool draw = m > -INFINITY && !greedy;
       if (m == -INFINITY) {   // nothing left to choose from
-        if (rank == 0 && threadIdx.x == 0) a.tokens[row] = -1, a.logps[row] = -INFINITY;
+        if (s.came && rank == 0 && threadIdx.x == 0) a.tokens[row] = -1, a.logps[row] = -INFINITY;
       } else if (greedy) {
         uint32_t best = 0xffffffffu;
 #pragma unroll
         for (int i = 0; i < kPer; i++)
           if (tops[i] == m) best = min(best, besides[i]);
         best = __reduce_min_sync(~0u, best);
-        if (rank == 0 && threadIdx.x == 0) a.tokens[row] = best, a.logps[row] = 0.0f;
+        if (s.came && rank == 0 && threadIdx.x == 0) a.tokens[row] = best, a.logps[row] = 0.0f;
       } else {
         s.m = m;
         s.c = __fdiv_rn(1.44269504f, temperature);
@@ -1233,7 +1258,10 @@ __global__ __launch_bounds__(W * 32, W == 8 || K == kFarSearch || (K == kFarPlai
         s.post(mine);
       }
 
-      if (bring) stream(next).bring_edges(edge, &sh.full[next % kB]);
+      if (bring) {
+        stream(next).bring_edges(edge, &sh.full[next % kB]);
+        if (lane == 0) sh.whole = next + 1;
+      }
       // the next row's first part, while the words of this one travel
       if (it + 1 < turns) look(it + 1);
 
@@ -1316,15 +1344,23 @@ __global__ __launch_bounds__(W * 32, W == 8 || K == kFarSearch || (K == kFarPlai
       if (!is_far(K) && lane == 0) bar_arrive(&sh.empty[it % kB]);
     }
     if (!s.ok) {
-      // a wait gave up: what is not done is marked, copies in flight land before the CTA goes
-      if (rank == 0 && threadIdx.x == 0)
-        for (; it < turns; it++) a.tokens[row_of(it)] = -1, a.logps[row_of(it)] = NAN;
-      for (int b = 0; b < kB; b++)
-        for (uint32_t parity = 0; parity < 2; parity++) bar_wait(&sh.full[b], parity);
+      // A wait gave up.  Which CTA has a row's token is not known here, so each
+      // marks the rows that it is not done with; where another was done with one,
+      // its token or logp may stand beside a mark.
+      if (threadIdx.x == 0)
+        for (uint32_t i = it; i < turns; i++) a.tokens[row_of(i)] = -1, a.logps[row_of(i)] = NAN;
+      // copies in flight land before the CTA goes
+      if (warp == 0) {
+        __syncwarp();
+        const uint32_t begun = sh.begun;
+        if (sh.whole < begun) stream(begun - 1).bring_edges(-INFINITY, &sh.full[(begun - 1) % kB]);
+        for (uint32_t i = begun > kB ? begun - kB : 0; i < begun; i++) bar_wait(&sh.full[i % kB], i / kB & 1);
+      }
     }
+    __syncwarp();
+    cluster_sync();
+    if (!s.ok) stay();
   }
-  __syncwarp();
-  cluster_sync();
 }
 
 constexpr int kDevices = 16;   // whose occupancy is kept (for a function, a number of CTAs and a buffer's size)
@@ -1401,7 +1437,7 @@ extern "C" int seqsum_sample_tokens(const void *logits, int32_t dtype, int64_t r
   if (rows == 0) return SEQSUM_OK;
   if (!u || !tokens || !logps || (vocab > 0 && !logits) || row_stride < 0) return SEQSUM_EINVAL;
   if (reinterpret_cast<uintptr_t>(logits) % (dtype == SEQSUM_FP32 ? 4 : 2)) return SEQSUM_EINVAL;
-  sq::SampleArgs a = {logits, rows, row_stride, (int32_t)vocab, u, *sampling, tokens, logps, 0};
+  sq::SampleArgs a = {logits, rows, row_stride, (int32_t)vocab, u, *sampling, tokens, logps, 0, sq::row::waits()};
   if (dtype == SEQSUM_FP32) return sq::choose_sample<float>(a, stream);
   if (dtype == SEQSUM_FP16) return sq::choose_sample<__half>(a, stream);
   return sq::choose_sample<__nv_bfloat16>(a, stream);

@@ -70,3 +70,60 @@ def test_logprob_with_next_to_no_limit(sq):
         sq.debug_set_fault(0, 0, 0)
         assert right_or_nan(lp, logps).all() and right_or_nan(ls, lses).all() and right_or_nan(out, d).all()
     assert torch.equal(sq.token_logprob_grad(x, t, a)[0], d)
+
+
+# ------------------------------------------------------------ sampling
+
+def sampling_settings(n):
+    i = torch.arange(n, device="cuda")
+    each = dict(temperature=torch.where(i % 5 == 0, 0.0, 0.5 + (i % 7) / 6.0).float(),
+                top_k=torch.where(i % 3 == 0, i % 100, 0).int(), top_p=torch.where(i % 4 == 1, 0.9, 1.0).float())
+    return [dict(), dict(temperature=0.0), dict(top_k=50), dict(top_p=0.9), dict(top_k=3000, top_p=0.8), each]
+
+
+def sample(sq, x, u, s, mode, arg, wait_ns):
+    n = x.shape[0]
+    tokens = torch.full((n,), -7, device="cuda", dtype=torch.int64)
+    logps = torch.full((n,), 7.0, device="cuda")
+    sq.debug_set_fault(mode, arg, wait_ns)
+    sq.sample_tokens(x, u, tokens=tokens, logps=logps, **s)
+    torch.cuda.synchronize()
+    sq.debug_set_fault(0, 0, 0)
+    return tokens, logps
+
+
+def check_sample(got, want):
+    (t, lp), (wt, wlp) = got, want
+    assert ((t == wt) | (t == -1)).all() and right_or_nan(lp, wlp).all(), (t, wt, lp, wlp)
+
+
+# one CTA a row; eight of 8 and of 16 warps (75 rows: two turns and four)
+@pytest.mark.parametrize("n,vocab,dtype,size,warps", [(3000, 5003, torch.bfloat16, 1, 8), (75, 131001, torch.float16, 8, 8),
+                                                      (75, 150001, torch.bfloat16, 8, 16)])
+@pytest.mark.parametrize("turn,warp", [(0, 0), (0, -1), (1, 3), (1, -1), (2, 0)])
+def test_sampling(sq, n, vocab, dtype, size, warps, turn, warp):
+    x, u, _ = logprob.make(n, vocab, dtype, 23)
+    u = torch.rand(n, device="cuda", generator=torch.Generator(device="cuda").manual_seed(24))
+    x[3] = -float("inf")
+    warp %= size * warps
+    for s in sampling_settings(n):
+        want = sq.sample_tokens(x, u, **s)
+        got = sample(sq, x, u, s, 2, turn * 128 + warp, LIMIT)
+        check_sample(got, want)
+        if turn < 2 or warps == 16 or size == 1:
+            assert got[0][-1] == -1 and got[1][-1].isnan()
+        if turn == 2:
+            assert got[0][0] == want[0][0] and got[1][0] == want[1][0]
+        again = sq.sample_tokens(x, u, **s)
+        assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
+
+
+def test_sampling_with_next_to_no_limit(sq):
+    x, u, _ = logprob.make(75, 131001, torch.bfloat16, 25)
+    u = torch.rand(75, device="cuda", generator=torch.Generator(device="cuda").manual_seed(26))
+    for s in sampling_settings(75):
+        want = sq.sample_tokens(x, u, **s)
+        for wait_ns in (1, 200, 1000, 3000, 10000):
+            check_sample(sample(sq, x, u, s, 0, 0, wait_ns), want)
+        again = sq.sample_tokens(x, u, **s)
+        assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
