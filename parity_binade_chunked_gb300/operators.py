@@ -73,12 +73,28 @@ def _call(index, stream, fn, *args):
         _check(rc)
 
 
+def _other(stream, device):
+    """`stream` as torch's, where it is given and not the current one; else None."""
+    if stream is None:
+        return None
+    handle = int(getattr(stream, "cuda_stream", stream))
+    if handle == _current_stream(device.index):
+        return None
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+
+
 def _new(shape, dtype, like, stream):
-    """An output's memory beside `like`; where another stream than the current one writes it, the allocator is told."""
-    t = torch.empty(shape, dtype=dtype, device=like.device)
-    if stream is not None:
-        t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
-                        torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream), device=like.device))
+    """An output's memory beside `like`.  Another stream than the current one takes it from its own memory: what the
+    current stream freed may still be in use there.  The current stream, which will read it, is noted."""
+    stream = _other(stream, like.device)
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    current = torch.cuda.current_stream(like.device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+    t.record_stream(current)
     return t
 
 
