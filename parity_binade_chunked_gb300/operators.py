@@ -3,8 +3,10 @@ log-probabilities and gradients, the norm of many tensors and clipping by it.
 
 The same thin binding as the package's: arguments are checked and passed on,
 every computation is a kernel of libseqsum.so.  Work is enqueued on the
-current torch stream unless a stream is given; results are ready once that
-stream reaches them.
+current torch stream unless a stream (or its handle) is given; results are
+ready once that stream reaches them.  A given stream is the caller's to order
+after the work that makes the inputs, and readers of the results after it;
+memory of inputs and results stays until the stream is through with it.
 """
 from __future__ import annotations
 
@@ -58,12 +60,18 @@ _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                           lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _call(index, stream, fn, *args):
-    """Calls an entry on device `index`, its last argument the stream's handle."""
+def _call(index, stream, used, fn, *args):
+    """Calls an entry on device `index`, its last argument the stream's handle.  Where that is not the current stream,
+    the memory of the tensors `used` is kept from others until the stream is through with the call."""
     if stream is None:
         handle = _current_stream(index)
     else:
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        other = _other(stream, torch.device("cuda", index))
+        if other is not None:
+            for t in used:
+                if isinstance(t, torch.Tensor):
+                    t.record_stream(other)
     if index == torch.cuda.current_device():
         rc = fn(*args, handle)
     else:
@@ -161,8 +169,8 @@ def sample_tokens(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tok
     up = _vector(u, "u", rows, torch.float32, index)
     tokens, tp = _output(tokens, "tokens", rows, torch.int64, index, logits, stream)
     logps, lp = _output(logps, "logps", rows, torch.float32, index, logits, stream)
-    _call(index, stream, _entries().seqsum_sample_tokens, logits.data_ptr(), dtype, rows, vocab, stride, up,
-          s, tp, lp)
+    _call(index, stream, (logits, u, temperature, top_k, top_p, min_p, tokens, logps), _entries().seqsum_sample_tokens,
+          logits.data_ptr(), dtype, rows, vocab, stride, up, s, tp, lp)
     return tokens, logps
 
 
@@ -174,7 +182,8 @@ def token_logprob(logits, tokens, logps=None, lses=None, stream=None):
     tp = _vector(tokens, "tokens", rows, torch.int64, index)
     logps, lp = _output(logps, "logps", rows, torch.float32, index, logits, stream)
     lses, sp = _output(lses, "lses", rows, torch.float32, index, logits, stream)
-    _call(index, stream, _entries().seqsum_token_logprob, logits.data_ptr(), dtype, rows, vocab, stride, tp, lp, sp)
+    _call(index, stream, (logits, tokens, logps, lses), _entries().seqsum_token_logprob, logits.data_ptr(), dtype, rows,
+          vocab, stride, tp, lp, sp)
     return logps, lses
 
 
@@ -201,8 +210,8 @@ def token_logprob_grad(logits, tokens, dlogps, out=None, logps=None, lses=None, 
     out, ostride = _gradient(out, logits, stream)
     logps, lp = _output(logps, "logps", rows, torch.float32, index, logits, stream)
     lses, sp = _output(lses, "lses", rows, torch.float32, index, logits, stream)
-    _call(index, stream, _entries().seqsum_token_logprob_grad, logits.data_ptr(), dtype, rows, vocab, stride, tp, gp,
-          out.data_ptr(), ostride, lp, sp)
+    _call(index, stream, (logits, tokens, dlogps, out, logps, lses), _entries().seqsum_token_logprob_grad,
+          logits.data_ptr(), dtype, rows, vocab, stride, tp, gp, out.data_ptr(), ostride, lp, sp)
     return out, logps, lses
 
 
@@ -214,8 +223,8 @@ def token_logprob_backward(logits, tokens, dlogps, lses, out=None, stream=None):
     gp = _vector(dlogps, "dlogps", rows, torch.float32, index)
     lp = _vector(lses, "lses", rows, torch.float32, index)
     out, ostride = _gradient(out, logits, stream)
-    _call(index, stream, _entries().seqsum_token_logprob_backward, logits.data_ptr(), dtype, rows, vocab, stride, tp, gp,
-          lp, out.data_ptr(), ostride)
+    _call(index, stream, (logits, tokens, dlogps, lses, out), _entries().seqsum_token_logprob_backward,
+          logits.data_ptr(), dtype, rows, vocab, stride, tp, gp, lp, out.data_ptr(), ostride)
     return out
 
 
@@ -282,14 +291,14 @@ class TensorList:
     def norm(self, scale: float = 1.0, out=None, stream=None):
         """scale * the 2-norm of all numbers of the list (a 1-element float32 tensor)."""
         out, p = self._out(out, stream)
-        _call(self._device.index, stream, _entries().seqsum_tensors_norm, self._h, scale, p)
+        _call(self._device.index, stream, (out,), _entries().seqsum_tensors_norm, self._h, scale, p)
         return out
 
     def clip(self, max_norm: float, scale: float = 1.0, out=None, stream=None):
         """Writes every number times scale * min(1, max_norm / (norm + 1e-6))
         and returns the norm (of the scaled numbers, before clipping)."""
         out, p = self._out(out, stream)
-        _call(self._device.index, stream, _entries().seqsum_tensors_clip, self._h, max_norm, scale, p)
+        _call(self._device.index, stream, (out,), _entries().seqsum_tensors_clip, self._h, max_norm, scale, p)
         return out
 
     def close(self):
