@@ -20,9 +20,9 @@ from . import build as _build
 __all__ = ["seqsum_f64", "seqsum_f64_static", "seqsum_f64_batched", "seqsum_f64_batched_sized", "get_stats",
            "debug_set_plan", "debug_set_fault", "debug_counters", "release_workspace", "version", "lib", "lib_path",
            "seqsum_f64_strided", "SeqsumPlan",
-           "SeqsumError", "sample_tokens", "token_logprob", "token_logprob_grad", "token_logprob_backward", "TensorList"]
+           "SeqsumError"]
 
-# loaded on first use, so that the package itself imports without torch
+# loaded on first use, so that the package, and `import *` of it, need no torch
 _OPERATORS = ("sample_tokens", "token_logprob", "token_logprob_grad", "token_logprob_backward", "TensorList")
 
 
@@ -33,6 +33,10 @@ def __getattr__(name):
             globals()[op] = getattr(operators, op)
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+def __dir__():
+    return sorted({*globals(), *_OPERATORS})
 
 
 _lock = threading.Lock()
