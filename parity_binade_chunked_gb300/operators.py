@@ -147,7 +147,8 @@ def sample_tokens(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tok
     (temperature, top_p, min_p float32, top_k int32).  temperature <= 0 is
     greedy; top_k <= 0, top_p >= 1 and min_p <= 0 are off.  The filters apply
     in the order top-k, top-p, min-p.  The sums are integers: a row's token
-    does not depend on the batch it is in."""
+    does not depend on the batch it is in.  The results have no history
+    (token_logprob's have)."""
     rows, vocab, stride, dtype, index = _logits(logits)
     s = _Sampling()
     if isinstance(temperature, torch.Tensor):
@@ -177,7 +178,21 @@ def sample_tokens(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tok
 def token_logprob(logits, tokens, logps=None, lses=None, stream=None):
     """(logps, lses), float32: the log-probability of each row's token and the
     row's log of the sum of exponentials.  A token outside [0, vocab) marks an
-    unused row: its logp is 0."""
+    unused row: its logp is 0.
+
+    Where autograd records and the logits require a gradient, logps has one:
+    its backward pass is token_logprob_backward.  There is none through lses
+    (a backward pass that needs it raises), and none into given results or on
+    another stream than the current one."""
+    if isinstance(logits, torch.Tensor) and logits.requires_grad and torch.is_grad_enabled():
+        if logps is not None or lses is not None or _other(stream, logits.device) is not None:
+            raise SeqsumError("seqsum: logits that require a gradient go with new results on the current stream "
+                              "(or detach them)")
+        return _TokenLogprob.apply(logits, tokens)
+    return _token_logprob(logits, tokens, logps, lses, stream)
+
+
+def _token_logprob(logits, tokens, logps, lses, stream):
     rows, vocab, stride, dtype, index = _logits(logits)
     tp = _vector(tokens, "tokens", rows, torch.int64, index)
     logps, lp = _output(logps, "logps", rows, torch.float32, index, logits, stream)
@@ -185,6 +200,25 @@ def token_logprob(logits, tokens, logps=None, lses=None, stream=None):
     _call(index, stream, (logits, tokens, logps, lses), _entries().seqsum_token_logprob, logits.data_ptr(), dtype, rows,
           vocab, stride, tp, lp, sp)
     return logps, lses
+
+
+class _TokenLogprob(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, tokens):
+        logps, lses = _token_logprob(logits, tokens, None, None, None)
+        ctx.save_for_backward(logits, tokens, lses)
+        ctx.set_materialize_grads(False)
+        return logps, lses
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dlogps, dlses):
+        if dlses is not None:
+            raise SeqsumError("seqsum: there is no gradient through the lses of token_logprob")
+        if dlogps is None:
+            return None, None
+        logits, tokens, lses = ctx.saved_tensors
+        return token_logprob_backward(logits, tokens, dlogps.contiguous(), lses), None
 
 
 def _gradient(out, logits, stream):
@@ -203,7 +237,8 @@ def _gradient(out, logits, stream):
 def token_logprob_grad(logits, tokens, dlogps, out=None, logps=None, lses=None, stream=None):
     """(dlogits, logps, lses): token_logprob and, from the same read of the
     logits, the gradient of (dlogps * logps).sum() with respect to them.
-    `out` may be the logits."""
+    `out` may be the logits.  The results have no history: the gradient is
+    there already, for logits.backward(dlogits) say."""
     rows, vocab, stride, dtype, index = _logits(logits)
     tp = _vector(tokens, "tokens", rows, torch.int64, index)
     gp = _vector(dlogps, "dlogps", rows, torch.float32, index)
@@ -217,7 +252,8 @@ def token_logprob_grad(logits, tokens, dlogps, out=None, logps=None, lses=None, 
 
 def token_logprob_backward(logits, tokens, dlogps, lses, out=None, stream=None):
     """dlogits: the gradient of (dlogps * logps).sum() with respect to the
-    logits, from the lses that token_logprob returned.  `out` may be the logits."""
+    logits, from the lses that token_logprob returned.  `out` may be the logits.
+    It has no history."""
     rows, vocab, stride, dtype, index = _logits(logits)
     tp = _vector(tokens, "tokens", rows, torch.int64, index)
     gp = _vector(dlogps, "dlogps", rows, torch.float32, index)
