@@ -131,12 +131,18 @@ def _number(v, name):
     return v
 
 
+# tells autograd that a given tensor is written, so that it finds saved ones that were overwritten
+_written = torch.autograd.graph.increment_version
+
+
 def _output(t, name, n, dtype, index, like, stream):
     """A given output, checked, or a new one: the tensor and its address."""
     if t is None:
         t = _new(n, dtype, like, stream)
         return t, t.data_ptr()
-    return t, _vector(t, name, n, dtype, index)
+    p = _vector(t, name, n, dtype, index)
+    _written(t)
+    return t, p
 
 
 def sample_tokens(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tokens=None, logps=None, stream=None):
@@ -231,6 +237,7 @@ def _gradient(out, logits, stream):
         raise TypeError("out must have the logits' shape, type and device")
     if rows > 1 and stride < vocab:
         raise TypeError("out's rows overlap")
+    _written(out)
     return out, stride
 
 
@@ -309,6 +316,7 @@ class TensorList:
             if o is not None:
                 entry.out, entry.out_dtype = o.data_ptr(), _DTYPES[o.dtype]
         self._keep = (tensors, outs)
+        self._clipped = [t if o is None else o for t, o in zip(tensors, outs)]
         self._device = device
         h = ctypes.c_void_p()
         with torch.cuda.device(device):
@@ -334,13 +342,14 @@ class TensorList:
         """Writes every number times scale * min(1, max_norm / (norm + 1e-6))
         and returns the norm (of the scaled numbers, before clipping)."""
         out, p = self._out(out, stream)
+        _written(self._clipped)
         _call(self._device.index, stream, (out,), _entries().seqsum_tensors_clip, self._h, max_norm, scale, p)
         return out
 
     def close(self):
         if self._h is not None:
             _entries().seqsum_tensors_destroy(self._h)
-        self._h = self._keep = None
+        self._h = self._keep = self._clipped = None
 
     def __del__(self):
         try:
