@@ -172,8 +172,12 @@ int seqsum_f64_planned(seqsum_plan *plan, const double *x, int64_t n, double s0,
 
 /* ---- Sums that decide: tokens, log-probabilities, the norm of gradients.
  *
- * Sums over rows of logits and over all gradients of a model, in the manner
- * of the sums above: their bits are defined.  The calls below enqueue on
+ * Sums over rows of logits and over all gradients of a model.  Sampling's are
+ * of integers and the norm's have one fixed order, so their bits do not depend
+ * on how the work is split or where it lies; a row's log-sum-exp is an fp32 sum
+ * whose order goes by the row's length, its type and its address modulo 16
+ * alone.  Exponentials are 2^x as the GPU gives it (ex2.approx, within about
+ * 2^-22 of itself), of an argument that is rounded to fp32.  The calls below enqueue on
  * `stream` and return without waiting, allocate nothing (seqsum_tensors_create
  * apart), use no workspace of a stream and may be captured into graphs.
  * seqsum_get_stats() does not cover them.  Their kernels' waits are bounded
@@ -205,7 +209,7 @@ typedef struct {
  * two tokens; here every sum is one of integers:
  *   m = the row's maximum (NaN counts as -inf), c = log2(e) / temperature
  *   d_i = (x_i - m) * c, w_i = 2^31 * 2^d_i rounded to an integer
- *   (d = 0 at the maximum; fp32 operations, each rounded)
+ *   (d = 0 at the maximum; fp32 operations, each rounded, 2^d as said above)
  *   order: larger d first, among equals the lower index
  *   top-k: the first k of the order; M = their sum of w
  *   top-p: an entry is kept where the sum before it is below floor(P * M / 2^32),
@@ -229,7 +233,9 @@ int seqsum_sample_tokens(const void *logits, int32_t dtype, int64_t rows, int64_
 /* For each row, lses[row] = ln sum exp(x_i) and logps[row] = x_token - lse.
  * A token outside [0, vocab) marks an unused row (padding): its logp is 0.  A
  * row of nothing but -inf has lse -inf and logp -inf; a NaN or +inf in a row
- * makes both NaN.  A row's results do not depend on the other rows. */
+ * makes both NaN.  A row's results do not depend on the other rows, but their
+ * last bits do on where the row begins within 16 bytes: rows of an odd vocab,
+ * one after another, begin at different places. */
 int seqsum_token_logprob(const void *logits, int32_t dtype, int64_t rows, int64_t vocab, int64_t row_stride,
                          const int64_t *tokens, float *logps, float *lses, cudaStream_t stream);
 

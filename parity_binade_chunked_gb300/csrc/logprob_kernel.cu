@@ -4,11 +4,14 @@
 //   lse = m + ln sum exp(x_i - m),  logp = x_t - lse,
 //   d logits_i = dlogp * ([i = t] - exp(x_i - lse))
 //
-// A row is cut into segments by its length alone, one for each warp that works
-// on it.  A segment's maximum and the
-// sum of its exponentials relative to that are formed by one warp in one
-// order, and the segments' sums are joined in one order: a row's results do
-// not depend on how many CTAs share it, so not on the other rows of the call.
+// A row's 16-byte vectors, counted from the aligned address at or below its
+// first number, are cut into segments, one for each warp that works on it.  A
+// segment's maximum and the sum of its exponentials relative to that are formed
+// by one warp in one order, and the segments' sums are joined in one order.  So
+// a row's results go by its numbers and its address modulo 16 alone, not by the
+// other rows of the call; at another place within 16 bytes other numbers share
+// a vector, and last bits may differ.  (Vectors counted from the row's first
+// number would end that, at the cost of a shift of every vector.)
 #include <math.h>
 
 #include <atomic>

@@ -1,7 +1,9 @@
-// Rows of logits on chip: a row is read once, in 16-byte vectors, by the CTAs
-// of one thread-block cluster, and stays there while it is reduced.  What the
-// kernels on rows share: element types, the parts of a row that a CTA or a
-// thread has, what the CTAs of a cluster tell each other, sums over warps.
+// What the kernels on rows of logits share: element types, the parts of a row
+// that a CTA or a thread has, what the CTAs of a cluster tell each other, sums
+// over warps.  Rows are read in 16-byte vectors: once, into registers (short
+// rows) or the shared memory of a cluster's CTAs, where they stay while they are
+// reduced; or, where many long rows are sampled and beyond what eight CTAs
+// hold, again from L2 for each pass.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -329,7 +331,8 @@ struct Slice {
 // first element, go to the lanes of a warp in steps of 32, and the steps are
 // cut into segments as even as can be, one for each warp of the cluster.
 // Where the cluster's size goes by the row's length alone, the same vectors
-// meet in one thread in the same order whatever else a call holds.
+// meet in one thread in the same order whatever else a call holds.  (Which
+// numbers share a vector goes by the row's address modulo 16.)
 //
 // What lies inside the row comes by one bulk copy; vectors that stick out of
 // it are put together from elements read one by one, with -inf beside them and
