@@ -165,13 +165,8 @@ __device__ __forceinline__ uint32_t ld_remote32(uint32_t a) {
 // Puts `v` of this CTA (the same in every thread) at box[rank] of every CTA
 // of the cluster and waits for theirs.
 __device__ __forceinline__ void cluster_post(uint64_t v, uint64_t *box, uint32_t rank, uint32_t size) {
-  if (size == 1) {
-    if (threadIdx.x == 0) box[0] = v;
-    __syncthreads();
-  } else {
-    if (threadIdx.x < size) st_remote(remote(&box[rank], threadIdx.x), v);
-    cluster_sync();
-  }
+  if (threadIdx.x < size) st_remote(remote(&box[rank], threadIdx.x), v);
+  cluster_sync();
 }
 
 // ---- reductions
@@ -271,36 +266,13 @@ struct Slice {
       for (int k = 0; k < KV; k++) keep[k] = read(k);
     }
   }
-  // the largest number of the slice; NaN is passed over
-  __device__ __forceinline__ float largest() const {
-    float m = -INFINITY;
-    if constexpr (KV > 0) {
-#pragma unroll
-      for (int k = 0; k < KV; k++)
-        if (k < steps) m = Elem<T>::vec_max(keep[k], m);
-    } else {
-      for (int k = 0; k < steps; k++) m = Elem<T>::vec_max(read(k), m);
-    }
-    return m;
-  }
-  // f(step, its elements as floats) for every step in index order
+  // f(step, its elements as floats) for every step in index order, read again
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
-    if constexpr (KV > 0) {
-#pragma unroll
-      for (int k = 0; k < KV; k++) {
-        if (k < steps) {
-          float x[kE];
-          Elem<T>::unpack(keep[k], x);
-          f(k, x);
-        }
-      }
-    } else {
-      for (int k = 0; k < steps; k++) {
-        float x[kE];
-        Elem<T>::unpack(read(k), x);
-        f(k, x);
-      }
+    for (int k = 0; k < steps; k++) {
+      float x[kE];
+      Elem<T>::unpack(read(k), x);
+      f(k, x);
     }
   }
   // writes a vector of the slice's place to another row of the same alignment or not

@@ -97,18 +97,6 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ uint32_t key_of(float d) { return __float_as_uint(d) & 0x7fffffffu; }
 
-// Sum over the CTA's threads, in every thread.  sh.warp is free again after the next barrier.
-template <int NT>
-__device__ __forceinline__ uint64_t block_sum(uint64_t v, Shared &sh) {
-  v = warp_sum(v);
-  if ((threadIdx.x & 31) == 0) sh.warp[threadIdx.x >> 5] = v;
-  __syncthreads();
-  uint64_t t = 0;
-#pragma unroll
-  for (int i = 0; i < NT / 32; i++) t += sh.warp[i];
-  return t;
-}
-
 // ---- rows too large for the buffers: one CTA a part of a row, every pass reads
 // global memory (L2), and every search goes over the whole row.
 
@@ -139,7 +127,7 @@ struct Sampler {
   // Sums the bins over the cluster and finds the first one at which the count
   // (or mass) reaches `need`; sh.bin = -1 where none does.
   __device__ void search(int level, bool by_mass, uint64_t need) {
-    if (size > 1) cluster_sync(); else __syncthreads();
+    cluster_sync();
     if (threadIdx.x < kBins) {
       uint32_t n = 0;
       uint64_t w = 0;
@@ -217,7 +205,7 @@ struct Sampler {
       const bool ties = hi - lo == 1;
       const uint32_t width = ties ? (uint32_t)(ihi - ilo) : hi - lo;
       const int shift = max(0, 32 - __clz(width - 1) - 8);
-      if (size > 1) cluster_sync(); else __syncthreads();   // everyone has read the bins of the split before
+      cluster_sync();   // everyone has read the bins of the split before
       clear(1);
       if (!ties) {
         entries([&](float d, int32_t) {
@@ -1366,7 +1354,7 @@ __global__ __launch_bounds__(W * 32, W == 8 || K == kFarSearch || (K == kFarPlai
 constexpr int kDevices = 16;   // whose occupancy is kept (for a function, a number of CTAs and a buffer's size)
 
 template <int W, Kind K>
-constexpr int kMostSteps = is_far(K) ? 1 : (int)(((226 << 10) - sizeof(Picks<W, K>)) / ((kBuffers<K> + (is_far(K))) * 32 * 16));
+constexpr int kMostSteps = is_far(K) ? 1 : (int)(((226 << 10) - sizeof(Picks<W, K>)) / (kBuffers<K> * 32 * 16));
 
 static_assert(kMostSteps<8, kSearch> * 32 * 8 < 1 << 16 && kMostSteps<16, kSearch> * 32 * 8 < 1 << 16,
               "the entries of a CTA's slice are counted in 16 bits, their mass of 2^31 each in 48");
