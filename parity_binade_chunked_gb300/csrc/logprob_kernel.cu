@@ -329,8 +329,11 @@ __global__ __launch_bounds__(kWarps * 32 + 32) void logprob_kernel(const Logprob
   if (!ok) stay();
 }
 
-// Short rows: a warp each, in registers; no barrier, no exchange.  (8192 x 3001 bf16 rows, gradient:
-// 29 us, the host's time; 46 us streamed.  4090: 49 and 51.)
+// Short rows: a warp each, in registers; no barrier, no exchange.  Bound by HBM,
+// where L2 does not hold the rows already: 8192 x 3001 bf16 27 us with gradient
+// (floor 14.5) and 17 without (7.3), L2 flushed; streamed 45 and 35.  With room
+// for 16 steps instead of 12 it takes 30 and 18.  (8192 x 4090, of 17 steps, is
+// streamed: 48 and 37.)
 template <typename T, int KV, bool kGrad>
 __global__ __launch_bounds__(128) void logprob_short_kernel(const LogprobArgs a) {
   constexpr int kE = Elem<T>::kPerVec;

@@ -25,9 +25,12 @@
 // wait for the cluster of about 1000 cycles (one row of 32000 bf16 numbers 6 and
 // 13 us); where they are many, issue slots and the latency of L2: an element
 // costs some 10 instructions a pass and there are two passes without filters,
-// four with.  256 x 131072 bf16 (floor 9.9 us): plain 24 us, top-k 50 42 us,
-// top-p 0.9 95 us, and 193 us at temperature 1.5, where the kept are 40000 of a
-// row and pass the lists; 512 x 131072 fp32 plain 80 us (floor 40).
+// four with.  256 x 131072 bf16 (floor 9.9 us): plain 24 us, greedy 15, min-p
+// 0.02 28, top-k 50 42, top-k 5000 175, top-p 0.9 95 us, and 193 us at
+// temperature 1.5, where the kept are 40000 of a row and pass the lists; 512 x
+// 131072 fp32 plain 80 us (floor 40).  The searches over rows in L2 run in 64
+// registers, two CTAs an SM, and spill some 400 bytes a thread.  (GPU time of
+// calls one after another in a graph.)
 #include <math.h>
 
 #include <atomic>
