@@ -58,6 +58,8 @@ def _entries():
 # the current stream's handle without a Stream object around it, where torch has that
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                           lambda index: torch.cuda.current_stream(index).cuda_stream)
+# the current device, where CUDA has been initialised (a tensor of it is at hand)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _call(index, stream, used, fn, *args):
@@ -72,7 +74,7 @@ def _call(index, stream, used, fn, *args):
             for t in used:
                 if isinstance(t, torch.Tensor):
                     t.record_stream(other)
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         rc = fn(*args, handle)
     else:
         with torch.cuda.device(index):
@@ -96,7 +98,8 @@ def _other(stream, device):
 def _new(shape, dtype, like, stream):
     """An output's memory beside `like`.  Another stream than the current one takes it from its own memory: what the
     current stream freed may still be in use there.  The current stream, which will read it, is noted."""
-    stream = _other(stream, like.device)
+    if stream is not None:
+        stream = _other(stream, like.device)
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=like.device)
     current = torch.cuda.current_stream(like.device)
