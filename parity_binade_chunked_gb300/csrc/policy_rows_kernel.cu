@@ -100,6 +100,8 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 // to where 2^d still is 0.  In 16 bits that is done to two numbers at once before
 // anything else, where the largest number lies far enough above the type's Low
 // (near_low); elsewhere to d.  Neither changes a bit of what other places give.
+// (A part without a number above -inf counts as one whose largest is 0: its
+// places, brought to Low, have to be far from that too, or their sum is not 0.)
 template <typename T>
 struct Low {
   static constexpr float value = 0.0f;
@@ -115,9 +117,9 @@ struct Low<__nv_bfloat16> {
   static constexpr uint32_t two = 0xf149f149u;
 };
 template <typename T>
-__device__ __forceinline__ bool near_low(float m, float c) {
+__device__ __forceinline__ bool near_low(float base, float c) {
   if constexpr (sizeof(T) == 4) return true;
-  return m > -INFINITY && !((m - Low<T>::value) * c > -kFar);
+  return !((base - Low<T>::value) * c > -kFar);
 }
 template <typename T, bool kNearLow>
 __device__ __forceinline__ uint4 within_reach(uint4 w) {
@@ -190,7 +192,7 @@ struct Part {
     for (int k = 0; k < N; k++) to = Elem<T>::vec_max(v[k], to);
     const float base = to == -INFINITY ? 0.0f : to;
     float t, u;
-    if (__any_sync(~0u, near_low<T>(to, c))) sums_of<T, N, true>(v, base, c, t, u);
+    if (__any_sync(~0u, near_low<T>(base, c))) sums_of<T, N, true>(v, base, c, t, u);
     else sums_of<T, N, false>(v, base, c, t, u);
     move(to, c);
     s += t, q += u;
@@ -613,7 +615,7 @@ __global__ __launch_bounds__(128, KV <= 8 ? 8 : 5) void short_rows_kernel(const 
 #pragma unroll
   for (int o = G / 2; o; o >>= 1) part.m = fmaxf(part.m, __shfl_xor_sync(~0u, part.m, o));
   const float base = part.m == -INFINITY ? 0.0f : part.m;
-  const bool near = __any_sync(~0u, near_low<T>(part.m, c));
+  const bool near = __any_sync(~0u, near_low<T>(base, c));
   auto add = [&](auto near) {
 #pragma unroll
     for (int k = 0; k < KV; k++) {
