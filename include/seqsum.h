@@ -362,7 +362,9 @@ int seqsum_policy_loss_backward(const float *logps, int64_t n, const seqsum_poli
  * is outside [0, vocab) is unused: its logits are not read, its gradient, logp and
  * entropy are 0.  A masked place (-inf) has p = 0 and gradient 0.  A used row of
  * nothing but -inf has logp -inf, entropy 0 and gradient 0; a NaN or +inf in a
- * row makes its logp, entropy and gradient NaN, and the loss.  Waits are bounded
+ * row makes its logp, entropy and gradient NaN, and the loss.  Where w entropy_coef /
+ * temperature passes 1e36, or g / temperature fp32's range, a row's gradient may be
+ * infinite or NaN, in masked places too.  Waits are bounded
  * as those of seqsum_token_logprob: one that gave up shows as NaN.
  *   dlogits  device, written, the logits' type; the logits themselves (with
  *            their stride) or memory apart from them

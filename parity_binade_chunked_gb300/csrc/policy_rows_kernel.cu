@@ -23,6 +23,7 @@ using namespace row;
 constexpr float kLn2 = 0.693147181f;
 // Octaves below the maximum at which 2^d is 0 whatever it is multiplied with; a masked place (d = -inf) counts as there.
 constexpr float kFar = -200.0f;
+constexpr float kMost = 1e38f;   // well inside fp32
 
 struct RowsArgs {
   const void *logits;
@@ -98,8 +99,9 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 }
 // A masked place has d = -inf, and 0 * -inf is NaN: it is brought within reach,
 // to where 2^d still is 0.  In 16 bits that is done to two numbers at once before
-// anything else, where the largest number lies far enough above the type's Low
-// (near_low); elsewhere to d.  Neither changes a bit of what other places give.
+// anything else, where the largest number lies far enough above the type's Low,
+// but not so far that d or its product with a factor passes fp32's range
+// (near_low: not so); elsewhere to d.  Neither changes a bit of what other places give.
 // (A part without a number above -inf counts as one whose largest is 0: its
 // places, brought to Low, have to be far from that too, or their sum is not 0.)
 template <typename T>
@@ -113,13 +115,14 @@ struct Low<__half> {
 };
 template <>
 struct Low<__nv_bfloat16> {
-  static constexpr float value = -0x1.92p99f;   // (some -1e30: c times the type's lowest would be -inf again)
+  static constexpr float value = -0x1.92p99f;   // (some -1e30: c times the type's lowest is -inf from c = 1 on)
   static constexpr uint32_t two = 0xf149f149u;
 };
 template <typename T>
-__device__ __forceinline__ bool near_low(float base, float c) {
+__device__ __forceinline__ bool near_low(float base, float c, float factor = 1.0f) {
   if constexpr (sizeof(T) == 4) return true;
-  return !((base - Low<T>::value) * c > -kFar);
+  const float d = (base - Low<T>::value) * c;
+  return !(d > -kFar && d < kMost && fabsf(factor) * d < kMost);
 }
 template <typename T, bool kNearLow>
 __device__ __forceinline__ uint4 within_reach(uint4 w) {
@@ -519,7 +522,7 @@ __global__ __launch_bounds__(kThreads<kWarps>) void rows_kernel(const RowsArgs a
       if (r.nothing) {
         zeros(x, row);
       } else {
-        by_kind<T>(bonus, near_low<T>(r.base, c), [&](auto bonus, auto near) {
+        by_kind<T>(bonus, near_low<T>(r.base, c, r.c1), [&](auto bonus, auto near) {
           write(x, own(x), row, [&](int32_t vec, float *y) {
             vec_gradient<T, decltype(bonus)::value, decltype(near)::value>(x.buf[vec], r, c, y);
           });
@@ -634,15 +637,16 @@ __global__ __launch_bounds__(128, KV <= 8 ? 8 : 5) void short_rows_kernel(const 
   Result r = result_of(a, t, part, xt);
   if (!used) r.logp = r.entropy = 0.0f;
   if (there && lane == 0) a.logps[row] = r.logp, a.entropies[row] = r.entropy;
+  const bool bonus = a.policy.entropy_coef != 0.0f;
+  if (!used || r.nothing) r.c0 = r.c1 = r.g = 0.0f;   // (2^-inf times that)
+  const bool clamp = bonus && __any_sync(~0u, near_low<T>(base, c, r.c1));
   __syncwarp();   // every lane of the row has its numbers: they may be overwritten
   if (!there) return;
   // (the exponentials are taken again: kept, they would cost the registers of the warps that hide the loads)
   asm volatile("" : "+f"(r.base));
-  if (!used || r.nothing) r.c0 = r.c1 = r.g = 0.0f;   // (2^-inf times that)
-  const bool bonus = a.policy.entropy_coef != 0.0f;
   T *d = static_cast<T *>(a.dlogits) + row * a.dstride;
   const bool aligned = same_alignment(d, off);
-  by_kind<T>(bonus, near, [&](auto bonus, auto near) {
+  by_kind<T>(bonus, clamp, [&](auto bonus, auto near) {
 #pragma unroll
     for (int k = 0; k < KV; k++) {
       const int32_t i = first + k * G * kE;
@@ -713,7 +717,7 @@ __global__ __launch_bounds__(NT) void reread_rows_kernel(const RowsArgs a) {
     write_zeros(x, d, aligned);
     return;
   }
-  by_kind<T>(a.policy.entropy_coef != 0.0f, near_low<T>(r.base, c), [&](auto bonus, auto near) {
+  by_kind<T>(a.policy.entropy_coef != 0.0f, near_low<T>(r.base, c, r.c1), [&](auto bonus, auto near) {
     for (int k = 0; k < x.steps; k++) {
       float y[x.kE];
       vec_gradient<T, decltype(bonus)::value, decltype(near)::value>(x.read(k), r, c, y);

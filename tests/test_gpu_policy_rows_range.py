@@ -96,3 +96,69 @@ def test_rows_of_nothing(sq, dtype, vocab, temperature):
         one = {k: v[r:r + 1].clone() for k, v in s.items() if v is not None}
         d, loss, stats, logps, h = sq.token_policy_grad(x[r:r + 1], t[r:r + 1].clone(), **one, **settings)
         assert logps.item() == -math.inf and h.item() == 0 and stats[2].item() == 0 and not d.any() and loss.isfinite()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("vocab", VOCABS)
+@pytest.mark.parametrize("temperature", [1e-30, 1e-20, 1e-12, 4e-9, 1e-6, 1e-3])
+@pytest.mark.parametrize("weight,entropy_coef,masked", [(1.0, 0.0, 0.0), (1.0, 0.05, 0.4), (65536.0, 0.05, 0.0),
+                                                        (65536.0, 0.01, 0.4)])
+def test_low_temperatures(sq, dtype, vocab, temperature, weight, entropy_coef, masked):
+    """Where the numbers' distances in octaves, and their products with the entropy's factor, pass fp32's range."""
+    settings = dict(entropy_coef=entropy_coef, temperature=temperature)
+    x, t, mask, s = make(8, vocab, dtype, 5, temperature, weight, masked)
+    x[3] = -math.inf     # used: nothing in it
+    x[5] = math.nan      # unused
+    s["weights"][5] = 0.0
+    d, loss, stats, logps, h = got = sq.token_policy_grad(x, t, **s, **settings)
+    assert logps[3].item() == -math.inf and not h[3].any() and not d[3].any()
+    assert not logps[5].any() and not h[5].any() and not d[5].any()
+    rest = torch.tensor([0, 1, 2, 4, 6, 7], device="cuda")
+    assert not d[rest][mask[rest]].any() and h.isfinite().all() and stats[2].isfinite() and not loss.isnan()
+    y = torch.where(x[:, :1].isfinite(), x, 0.0)
+    check(y, t, {**s, "weights": s["weights"].index_fill(0, torch.tensor([3], device="cuda"), 0.0)}, settings, got, rest, loss=False)
+    # the sums, without the row whose logp has no end
+    s["weights"][3] = 0.0
+    check(y, t, s, settings, sq.token_policy_grad(x, t, **s, **settings), rest)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("vocab", VOCABS)
+@pytest.mark.parametrize("temperature", [1e-30, 1e-3, 1.0, 1e4, 1e30])
+@pytest.mark.parametrize("entropy_coef", [0.0, 0.1])
+def test_extreme_numbers(sq, dtype, vocab, temperature, entropy_coef):
+    """Rows of one number, of the type's lowest, with its largest, with NaN and +inf, in every kernel and type."""
+    settings = dict(entropy_coef=entropy_coef, temperature=temperature)
+    x, t, _, s = make(9, vocab, dtype, 6, temperature)
+    least, most = torch.finfo(dtype).min, torch.finfo(dtype).max
+    x[0, 1:] = -math.inf               # one number
+    x[1] = least                       # the lowest, all of it
+    x[2] = -math.inf
+    x[2, ::2] = least                  # and half of it, the rest masked
+    x[3, 1:] = least                   # beside an ordinary one
+    x[4, 0] = most                     # the largest beside ordinary and masked ones
+    x[4, 1::3] = -math.inf
+    x[5, 2] = math.nan
+    x[6, 2] = math.inf
+    x[7, 1], t[7] = -math.inf, 1       # a masked token
+    t[:5] = 0
+    s["weights"][8] = 0.0
+    s["old_logps"][:5] = -0.1
+    s["old_logps"][1:3] = -math.log(vocab) + 0.1
+    d, loss, stats, logps, h = got = sq.token_policy_grad(x, t, **s, **settings)
+    assert loss.isnan() and stats[2].isnan()
+    for r in (5, 6):
+        assert logps[r].isnan() and h[r].isnan() and d[r].isnan().all()
+    assert logps[0].item() == 0 and h[0].item() == 0 and not d[0, 1:].any()
+    assert logps[7].item() == -math.inf and d[7, 1].item() == 0 and not d[8].any() and not h[8].any()
+    for r in (0, 2, 4, 7):
+        assert not d[r][x[r] == -math.inf].any()
+    s["weights"][5:7] = 0.0
+    finite = x.nan_to_num(nan=0.0, neginf=-math.inf, posinf=0.0)
+    rest = torch.tensor([0, 1, 2, 3, 4], device="cuda")
+    check(finite, t, s, settings, got, rest, loss=False)
+    # nothing beside the bad rows knows of them
+    again = sq.token_policy_grad(x, t, **s, **settings)
+    keep = torch.tensor([0, 1, 2, 3, 4, 7, 8], device="cuda")
+    assert all(torch.equal(again[k][keep], got[k][keep]) for k in (0, 3, 4))
+    assert again[2][:4].isfinite().all()   # (of the old policy's KL row 7 has one without end)
