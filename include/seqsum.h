@@ -501,7 +501,9 @@ int seqsum_debug_counters(unsigned long long *out, int n);
  * calls of seqsum_sample_tokens, seqsum_token_logprob and _grad and
  * seqsum_token_policy_grad, where they stream rows through shared memory, warp
  * arg % 128 of each cluster takes its wait for the cluster's row number arg / 128
- * (of used rows, for the last of these) as given up.
+ * (of used rows, for the last of these) as given up.  Mode 3: the sums of later
+ * policy losses of up to 65536 tokens take clusters of at most `arg` CTAs (1 to 16),
+ * as on a GPU that has no room for larger ones.
  * Returns SEQSUM_OK or SEQSUM_EINVAL. */
 int seqsum_debug_set_fault(int mode, int64_t arg, int64_t wait_ns);
 

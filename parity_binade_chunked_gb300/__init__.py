@@ -310,7 +310,7 @@ def debug_read(n: int = 64) -> list:
 def debug_set_fault(mode: int, arg: int = 0, wait_ns: int = 0) -> None:
     """Test hook for the bounded device waits: mode 1 withholds the header of
     tile `arg` in later calls; mode 2 lets a warp's wait for a row of logits
-    give up (see the header); wait_ns > 0 shortens every wait (0: 2 s)."""
+    give up, mode 3 keeps a policy loss's clusters small (see the header); wait_ns > 0 shortens every wait (0: 2 s)."""
     _check(lib().seqsum_debug_set_fault(int(mode), int(arg), int(wait_ns)))
 
 

@@ -9,7 +9,8 @@
 // The tokens are cut into chunks of four a thread, the chunks into groups; their
 // sizes go by the number of tokens alone.  A thread adds its tokens in order, the
 // threads of a warp, the warps and the groups are joined by trees: a sum's order
-// does not depend on the GPU or on what else runs.
+// does not depend on the GPU or on what else runs (a cluster that has fewer CTAs
+// than there are groups takes them in turns).
 #include "policy_terms.cuh"
 
 #include <atomic>
@@ -21,7 +22,7 @@ namespace loss {
 namespace {
 
 constexpr int kThreads = 256, kMostThreads = 512;   // of a CTA; of one of a cluster for more tokens
-constexpr int kMostCtas = 16;                      // of a cluster, where the GPU has room for such
+constexpr int kMostGroups = 16;                    // of a cluster, a CTA each where the GPU has room for such clusters
 constexpr int kCtas = 3;                               // of an SM
 constexpr int kGroups = 152 * kCtas;              // at most: all at once on this GPU
 constexpr int kSums = 6;                          // policy, kl, entropy, past, old kl, weight
@@ -161,59 +162,65 @@ template <bool kValue, bool kGrad, bool kCluster, int kThr>
 __global__ __launch_bounds__(kThr, kCluster ? 1 : kCtas) void tokens_kernel(const TokensArgs a) {
   constexpr int kWarps = kThr / 32;
   constexpr int64_t kChunk = kThr * 4;
-  __shared__ uint64_t box[kSums][(kCluster ? kMostCtas : 1) * kWarps];
+  __shared__ uint64_t box[kSums][(kCluster ? kMostGroups : 1) * kWarps];
   __shared__ uint64_t total[kSums];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t size = kCluster ? row::cluster_size() : 1, rank = kCluster ? row::cluster_rank() : 0;
   if (kCluster) row::cluster_begun();
   // (finish_kernel may come onto an SM, and waits for the end of this one)
   if (kValue && !kCluster) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int64_t from = a.chunks * blockIdx.x / a.groups, to = a.chunks * (blockIdx.x + 1) / a.groups;
   auto place = [&](int64_t chunk) { return chunk * kChunk + threadIdx.x * 4; };
-  Beside b = {};
-  if (from < to) {
-    b.w = load_weights(a, place(from));
-    load_rest(a, place(from), b);
-  }
-  // (the kernel before writes nothing of what has been read so far)
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const float dloss = kGrad && a.dloss ? *a.dloss : 1.0f;
-  TwoSums first;
-  Sum sums[kSums];
-  for (int64_t c = from; c < to; c++) {
-    float4 lp = {}, h = {}, next = {};
-    if (any(b.w)) {
-      lp = load4(a.logps, place(c), a.n, a.vectors);
-      if (kValue && a.entropies) h = load4(a.entropies, place(c), a.n, a.vectors);
+  uint32_t group = blockIdx.x;
+  do {   // (one, but for a cluster of fewer CTAs than groups)
+    const int64_t from = a.chunks * group / a.groups, to = a.chunks * (group + 1) / a.groups;
+    Beside b = {};
+    if (from < to) {
+      b.w = load_weights(a, place(from));
+      load_rest(a, place(from), b);
     }
-    if (c + 1 < to) next = load_weights(a, place(c + 1));   // here before the chunk that asks for them
-    four_tokens<kValue, kGrad>(a, place(c), b, lp, h, dloss, first, sums);
-    b.w = next;
-    if (c + 1 < to) load_rest(a, place(c + 1), b);
-  }
-  if constexpr (kValue) {
-    Sum other;
-    first.get(sums[0], other);
-    sums[0].add(other);
-    __syncwarp();
-    if (kCluster) row::cluster_wait_begun();
+    // (the kernel before writes nothing of what has been read so far)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const float dloss = kGrad && a.dloss ? *a.dloss : 1.0f;
+    TwoSums first;
+    Sum sums[kSums];
+    for (int64_t c = from; c < to; c++) {
+      float4 lp = {}, h = {}, next = {};
+      if (any(b.w)) {
+        lp = load4(a.logps, place(c), a.n, a.vectors);
+        if (kValue && a.entropies) h = load4(a.entropies, place(c), a.n, a.vectors);
+      }
+      if (c + 1 < to) next = load_weights(a, place(c + 1));   // here before the chunk that asks for them
+      four_tokens<kValue, kGrad>(a, place(c), b, lp, h, dloss, first, sums);
+      b.w = next;
+      if (c + 1 < to) load_rest(a, place(c + 1), b);
+    }
+    if constexpr (kValue) {
+      Sum other;
+      first.get(sums[0], other);
+      sums[0].add(other);
+      __syncwarp();
+      if (kCluster && group == blockIdx.x) row::cluster_wait_begun();
 #pragma unroll
-    for (int k = 0; k < kSums; k++) {
-      const Sum s = warp_add(sums[k]);
-      if (lane == 0) {
-        if (kCluster) row::st_remote(row::remote(&box[k][rank * kWarps + warp], 0), row::pair(s.hi, s.lo));
-        else box[k][warp] = row::pair(s.hi, s.lo);
+      for (int k = 0; k < kSums; k++) {
+        const Sum s = warp_add(sums[k]);
+        if (lane == 0) {
+          if (kCluster) row::st_remote(row::remote(&box[k][group * kWarps + warp], 0), row::pair(s.hi, s.lo));
+          else box[k][warp] = row::pair(s.hi, s.lo);
+        }
       }
     }
+    group += gridDim.x;
+  } while (kCluster && group < (uint32_t)a.groups);
+  if constexpr (kValue) {
     __syncwarp();
     if (kCluster && size > 1) row::cluster_sync();
     else __syncthreads();
     if (rank != 0) return;
     Sum s;
     if (warp < kSums) {
-      const int n = (int)size * kWarps;
+      const int n = (kCluster ? a.groups : 1) * kWarps;
 #pragma unroll
-      for (int k = 0; k < (kCluster ? kMostCtas : 1) * kWarps; k += 32) {
+      for (int k = 0; k < (kCluster ? kMostGroups : 1) * kWarps; k += 32) {
         Sum t;
         if (lane + k < n) row::split(box[warp][lane + k], t.hi, t.lo);
         s.add(t);
@@ -245,32 +252,32 @@ __global__ __launch_bounds__(kSums * 32) void finish_kernel(const TokensArgs a) 
   write_loss(a, warp_add(s), total);
 }
 
-// The largest cluster of a kernel that the current device takes: 16 CTAs, or the portable eight.
+// The largest cluster of a kernel that the current device takes: 16 CTAs, or the portable eight (or fewer for a test).
 template <void (*kernel)(const TokensArgs), int threads>
 int widest() {
   constexpr int kDevices = 16;
   static std::atomic<int> known[kDevices];
   int device = 0;
-  if (cudaGetDevice(&device) != cudaSuccess || device >= kDevices) return row::kMaxCluster;
+  if (cudaGetDevice(&device) != cudaSuccess || device >= kDevices) return min(row::kMaxCluster, row::most_ctas());
   int size = known[device].load(std::memory_order_relaxed);
   if (size == 0) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kMostCtas);
+    cfg.gridDim = dim3(kMostGroups);
     cfg.blockDim = dim3(threads);
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = kMostCtas;
+    at[0].val.clusterDim.x = kMostGroups;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
     int n = 0;
     size = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
                    cudaOccupancyMaxActiveClusters(&n, (const void *)kernel, &cfg) == cudaSuccess && n > 0
-               ? kMostCtas
+               ? kMostGroups
                : row::kMaxCluster;
     known[device].store(size, std::memory_order_relaxed);
   }
-  return size;
+  return min(size, row::most_ctas());
 }
 
 bool aligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -288,9 +295,10 @@ int run_tokens(TokensArgs &a, bool after, cudaStream_t stream) {
   if (kValue && a.n <= kClusterTokens) {
     const int most = threads == kThreads ? widest<tokens_kernel<kValue, kGrad, true, kThreads>, kThreads>()
                                          : widest<tokens_kernel<kValue, kGrad, true, kMostThreads>, kMostThreads>();
+    a.groups = 1;
+    while (a.groups < kMostGroups && a.groups < a.chunks) a.groups *= 2;
     int size = 1;
-    while (size < most && size < a.chunks) size *= 2;
-    a.groups = size;
+    while (2 * size <= most && size < a.groups) size *= 2;
     e = threads == kThreads ? launch_after(tokens_kernel<kValue, kGrad, true, kThreads>, a, size, kThreads, size, after, stream)
                             : launch_after(tokens_kernel<kValue, kGrad, true, kMostThreads>, a, size, kMostThreads, size, after, stream);
   } else {

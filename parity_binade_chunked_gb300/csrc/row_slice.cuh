@@ -23,6 +23,8 @@ namespace row {
 struct Waits;
 // What the next call's waits are given (seqsum_debug_set_fault).
 Waits waits();
+// The largest cluster that later sums over tokens may take (the same hook).
+int most_ctas();
 
 constexpr int kMaxCluster = 8;           // the portable cluster size
 constexpr int64_t kMaxVocab = 1 << 24;   // element indices fit 32 bits, 2^24 weights of 2^31 fit 64

@@ -18,3 +18,9 @@ def test_modes(hook):
     assert hook(0, 0, 0) == hook(1, 5, 1000) == hook(2, 3 * 128 + 7, 1 << 40) == 0
     for bad in ((-1, 0, 0), (3, 0, 0), (0, 0, -1), (2, -1, 0), (2, 1 << 34, 0)):
         assert hook(*bad) == -1
+
+
+def test_cluster_sizes(hook):
+    assert hook(3, 1, 0) == hook(3, 16, 0) == hook(0, 0, 0) == 0
+    for arg in (-1, 0, 17, 1 << 40):
+        assert hook(3, arg, 0) == -1
