@@ -14,7 +14,7 @@ import math
 import torch
 
 from . import SeqsumError, lib
-from .operators import _call, _gradient, _logits, _new, _other, _output, _vector
+from .operators import _call, _gradient, _logits, _new, _no_tangents, _other, _output, _vector
 
 _SCRATCH = 49152           # SEQSUM_POLICY_SCRATCH
 _NO_SCRATCH = 65536        # tokens that need none
@@ -134,8 +134,10 @@ def policy_loss(logps, old_logps, advantages, weights, ref_logps=None, clip_low=
 
     Where autograd records and logps require a gradient, loss has one.  There is
     none through stats or into the other tensors, and none into given results or
-    on another stream than the current one."""
+    on another stream than the current one; tensors with a forward-mode tangent
+    are refused."""
     settings = (clip_low, clip_high, max_ratio, kl_coef, 0.0, 1.0)
+    _no_tangents(logps=logps, old_logps=old_logps, advantages=advantages, weights=weights, ref_logps=ref_logps)
     _constant(old_logps=old_logps, advantages=advantages, weights=weights, ref_logps=ref_logps)
     if _recorded(logps, (loss, stats), stream, "logps"):
         return _PolicyLoss.apply(logps, old_logps, advantages, weights, ref_logps, settings)
@@ -244,8 +246,10 @@ def preference_loss(logps, offsets, ref_logps=None, weights=None, kind="sigmoid"
 
     Where autograd records and logps require a gradient, loss has one.  There is
     none through scores or into the other tensors, and none into given results or
-    on another stream than the current one."""
+    on another stream than the current one; tensors with a forward-mode tangent
+    are refused."""
     settings = _preference(kind, beta, margin, smoothing, average)
+    _no_tangents(logps=logps, ref_logps=ref_logps, weights=weights)
     _constant(ref_logps=ref_logps, weights=weights)
     if _recorded(logps, (loss, scores), stream, "logps"):
         return _PreferenceLoss.apply(logps, offsets, ref_logps, weights, settings)

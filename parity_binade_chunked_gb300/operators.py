@@ -148,6 +148,18 @@ def _output(t, name, n, dtype, index, like, stream):
     return t, p
 
 
+_forward = torch.autograd.forward_ad
+
+
+def _no_tangents(**named):
+    """Refuses tensors of forward-mode differentiation, whose tangents a call would lose."""
+    if getattr(_forward, "_current_level", 0) < 0:   # (no such differentiation is under way)
+        return
+    for name, t in named.items():
+        if isinstance(t, torch.Tensor) and _forward.unpack_dual(t).tangent is not None:
+            raise SeqsumError(f"seqsum: there is no forward-mode derivative through {name} (detach it)")
+
+
 def sample_tokens(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tokens=None, logps=None, stream=None):
     """One token a row of `logits` (rows x vocab) from the random numbers `u`
     (float32, one a row, in [0, 1)): (tokens int64, logps float32).
@@ -192,7 +204,9 @@ def token_logprob(logits, tokens, logps=None, lses=None, stream=None):
     Where autograd records and the logits require a gradient, logps has one:
     its backward pass is token_logprob_backward.  There is none through lses
     (a backward pass that needs it raises), and none into given results or on
-    another stream than the current one."""
+    another stream than the current one.  Logits with a forward-mode tangent are
+    refused."""
+    _no_tangents(logits=logits)
     if isinstance(logits, torch.Tensor) and logits.requires_grad and torch.is_grad_enabled():
         if logps is not None or lses is not None or _other(stream, logits.device) is not None:
             raise SeqsumError("seqsum: logits that require a gradient go with new results on the current stream "
