@@ -300,8 +300,8 @@ int seqsum_tensors_clip(seqsum_tensors *tensors, float max_norm, float scale, fl
  * goes by the number of tokens, or the lengths of the sequences, alone.  Values
  * of single tokens are fp32.  The calls enqueue on `stream` and return without
  * waiting, allocate nothing, use no workspace of a stream and may be captured
- * into graphs.  What a call writes must not overlap what it reads, but where
- * that is said. */
+ * into graphs.  What a call writes must not overlap what it reads or what else
+ * it writes, but where that is said: SEQSUM_EINVAL. */
 
 /* The largest number of tokens of one call. */
 #define SEQSUM_MAX_TOKENS ((int64_t)1 << 40)
@@ -368,7 +368,7 @@ int seqsum_policy_loss_backward(const float *logps, int64_t n, const seqsum_poli
  * as those of seqsum_token_logprob: one that gave up shows as NaN.
  *   dlogits  device, written, the logits' type; the logits themselves (with
  *            their stride) or memory apart from them
- *   logps, entropies  device, one a row, written: two places, neither that of a vector of `policy`
+ *   logps, entropies  device, one a row, written
  *   loss, stats  as above (stats[2]: the entropies')
  *   scratch  as above, for rows */
 int seqsum_token_policy_grad(const void *logits, int32_t dtype, int64_t rows, int64_t vocab, int64_t row_stride,

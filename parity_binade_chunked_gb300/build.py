@@ -21,7 +21,7 @@ CHECK_BUILD = os.path.join(BUILD, "check")
 CHECK_LIB = os.path.join(CHECK_BUILD, "libseqsum.so")
 SOURCES = ["seqsum_kernel.cu", "seqsum_api.cu", "seqsum_static.cu", "sample_kernel.cu", "logprob_kernel.cu",
            "tensors_kernel.cu", "policy_kernel.cu", "policy_rows_kernel.cu", "preference_kernel.cu"]
-HEADERS = ["binade_math.cuh", "seqsum_internal.cuh", "row_slice.cuh", "row_exp.cuh", "policy_terms.cuh"]
+HEADERS = ["binade_math.cuh", "seqsum_internal.cuh", "row_slice.cuh", "row_exp.cuh", "policy_terms.cuh", "places.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "--fmad=false", "-std=c++17", "-Xcompiler", "-fPIC",
                      "-Xcompiler", "-fno-fast-math", "-Xcompiler", "-ffp-contract=off",

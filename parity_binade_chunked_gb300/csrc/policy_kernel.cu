@@ -353,6 +353,14 @@ int seqsum_policy_loss(const float *logps, int64_t n, const seqsum_policy *polic
   if (sq::loss::misplaced(logps) || sq::loss::misplaced(dlogps) || sq::loss::misplaced(loss) || sq::loss::misplaced(stats) ||
       reinterpret_cast<uintptr_t>(scratch) % sizeof(float2))
     return SEQSUM_EINVAL;
+  const sq::loss::Policy &p = a.policy;
+  const int64_t bytes = n * (int64_t)sizeof(float);
+  using sq::loss::place;
+  if (!sq::loss::apart({place(dlogps, bytes), place(loss, sizeof(float)), place(stats, 6 * sizeof(float)),
+                        place(scratch, n > sq::loss::kClusterTokens ? SEQSUM_POLICY_SCRATCH : 0)},
+                       {place(logps == dlogps ? nullptr : logps, bytes), place(p.old_logps, bytes), place(p.advantages, bytes),
+                        place(p.weights, bytes), place(p.ref_logps, bytes)}))
+    return SEQSUM_EINVAL;
   a.logps = logps, a.n = n, a.dlogps = dlogps, a.loss = loss, a.stats = stats, a.scratch = static_cast<float2 *>(scratch);
   return dlogps ? sq::loss::run_tokens<true, true>(a, false, stream) : sq::loss::run_tokens<true, false>(a, false, stream);
 }
@@ -362,6 +370,13 @@ int seqsum_policy_loss_backward(const float *logps, int64_t n, const seqsum_poli
   sq::loss::TokensArgs a = {};
   if (!sq::loss::take_policy(policy, n, false, &a.policy) || (n > 0 && (!logps || !dlogps || !dloss))) return SEQSUM_EINVAL;
   if (sq::loss::misplaced(logps) || sq::loss::misplaced(dlogps) || sq::loss::misplaced(dloss)) return SEQSUM_EINVAL;
+  const sq::loss::Policy &p = a.policy;
+  const int64_t bytes = n * (int64_t)sizeof(float);
+  using sq::loss::place;
+  if (!sq::loss::apart({place(dlogps, bytes)}, {place(logps == dlogps ? nullptr : logps, bytes), place(dloss, sizeof(float)),
+                                                place(p.old_logps, bytes), place(p.advantages, bytes), place(p.weights, bytes),
+                                                place(p.ref_logps, bytes)}))
+    return SEQSUM_EINVAL;
   a.logps = logps, a.n = n, a.dlogps = dlogps, a.dloss = dloss;
   return sq::loss::run_tokens<false, true>(a, false, stream);
 }

@@ -807,12 +807,20 @@ extern "C" int seqsum_token_policy_grad(const void *logits, int32_t dtype, int64
     if (reinterpret_cast<uintptr_t>(out) % sizeof(float)) return SEQSUM_EINVAL;
   if (reinterpret_cast<uintptr_t>(scratch) % sizeof(float2)) return SEQSUM_EINVAL;
   if (rows > 0) {
-    if (!tokens || !logps || !entropies || logps == entropies || (rows > 1 && drow_stride < vocab)) return SEQSUM_EINVAL;
+    if (!tokens || !logps || !entropies || (rows > 1 && drow_stride < vocab)) return SEQSUM_EINVAL;
     if (!scratch && rows > loss::kClusterTokens) return SEQSUM_EINVAL;
-    // the loss is taken from the log-probabilities and the tokens' numbers once these are written
+    // the loss is taken from the log-probabilities and the tokens' numbers once these and the gradient are written
     const loss::Policy &p = a.policy;
-    for (const float *in : {p.old_logps, p.advantages, p.weights, p.ref_logps})
-      if (in == logps || in == entropies) return SEQSUM_EINVAL;
+    const int64_t size = dtype == SEQSUM_FP32 ? 4 : 2, bytes = rows * (int64_t)sizeof(float);
+    const bool in_place = dlogits == logits && (rows == 1 || drow_stride == row_stride);
+    using loss::place;
+    if (!loss::apart({place(dlogits, rows, (__int128)drow_stride * size, vocab * size), place(logps, bytes), place(entropies, bytes),
+                      place(loss, sizeof(float)), place(stats, 6 * sizeof(float)),
+                      place(scratch, rows > loss::kClusterTokens ? SEQSUM_POLICY_SCRATCH : 0)},
+                     {place(in_place ? nullptr : logits, rows, (__int128)row_stride * size, vocab * size),
+                      place(tokens, rows * (int64_t)sizeof(int64_t)), place(p.old_logps, bytes), place(p.advantages, bytes),
+                      place(p.weights, bytes), place(p.ref_logps, bytes)}))
+      return SEQSUM_EINVAL;
     const cudaError_t e = dtype == SEQSUM_FP32   ? launch_policy_rows<float>(a, stream)
                           : dtype == SEQSUM_FP16 ? launch_policy_rows<__half>(a, stream)
                                                  : launch_policy_rows<__nv_bfloat16>(a, stream);

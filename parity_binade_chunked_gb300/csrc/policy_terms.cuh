@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "../../include/seqsum.h"
+#include "places.h"
 #include "row_slice.cuh"
 
 namespace sq {

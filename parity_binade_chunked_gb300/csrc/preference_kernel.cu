@@ -541,6 +541,11 @@ int seqsum_preference_loss(const float *logps, const float *ref_logps, const flo
   for (const float *p : {logps, ref_logps, weights, (const float *)dlogps, (const float *)loss, (const float *)scores,
                          (const float *)slopes, (const float *)losses})
     if (misplaced(p)) return SEQSUM_EINVAL;
+  const int64_t bytes = n * (int64_t)sizeof(float), each = pairs * (int64_t)sizeof(float);
+  if (!apart({place(dlogps, bytes), place(loss, sizeof(float)), place(scores, 2 * each), place(slopes, 2 * each), place(losses, each)},
+             {place(logps == dlogps ? nullptr : logps, bytes), place(ref_logps, bytes), place(weights, bytes),
+              place(offsets, (2 * pairs + 1) * (int64_t)sizeof(int64_t))}))
+    return SEQSUM_EINVAL;
   const PairsArgs a = {logps, ref_logps, weights, n, offsets, pairs, pair_of(s->beta), pair_of(s->margin),
                        pair_of(0.5 / s->beta), (float)s->smoothing,
                        pairs > 0 ? (float)(1.0 / (double)pairs) : 0.0f, s->kind,
@@ -553,6 +558,10 @@ int seqsum_preference_backward(const float *weights, int64_t n, const int64_t *o
   using namespace sq::loss;
   if (bad_pairs(n, offsets, pairs) || (n > 0 && (!dloss || !dlogps)) || (pairs > 0 && !slopes)) return SEQSUM_EINVAL;
   if (misplaced(weights) || misplaced(slopes) || misplaced(dloss) || misplaced(dlogps)) return SEQSUM_EINVAL;
+  if (!apart({place(dlogps, n * (int64_t)sizeof(float))},
+             {place(weights, n * (int64_t)sizeof(float)), place(offsets, (2 * pairs + 1) * (int64_t)sizeof(int64_t)),
+              place(slopes, 2 * pairs * (int64_t)sizeof(float)), place(dloss, sizeof(float))}))
+    return SEQSUM_EINVAL;
   PairsArgs a = {};
   a.weights = weights, a.n = n, a.offsets = offsets, a.pairs = pairs, a.slopes = const_cast<float *>(slopes);
   a.dloss = dloss, a.dlogps = dlogps;

@@ -108,12 +108,21 @@ def _scratch(n, like, stream):
     return t, t.data_ptr()
 
 
-def _apart(out, inputs):
-    """Refuses results in the place of vectors that are still read, or of each other."""
-    for name, t in out:
-        for other, x in inputs:
-            if t is not None and x is not None and t.data_ptr() == x.data_ptr() and x.numel() > 0:
-                raise ValueError(f"{name} and {other} are the same memory")
+def _overlap(names, written, in_place, used):
+    """After a refusal: names a result, of the first `written` of the tensors `used`, that lies in the memory of another
+    of them, if there is one (out may be the tensor called `in_place`)."""
+    spans = []
+    for name, t in zip(names, used):
+        first = last = 0
+        if t is not None and t.numel() > 0:
+            first = t.data_ptr()
+            last = first + t.element_size() * (1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride())))
+        spans.append((name, first, last))
+    for name, first, last in spans[:written]:
+        for other, start, end in spans:
+            if other != name and first < end and start < last and not (
+                    name == "out" and other == in_place and (first, last) == (start, end)):
+                raise ValueError(f"{name} and {other} are the same memory, or overlap") from None
 
 
 def policy_loss(logps, old_logps, advantages, weights, ref_logps=None, clip_low=0.2, clip_high=0.2, max_ratio=math.inf,
@@ -162,8 +171,12 @@ def _policy_loss(logps, old_logps, advantages, weights, ref_logps, settings, out
     loss, lp = _result(loss, "loss", 1, logps, index, stream)
     stats, sp = _result(stats, "stats", 6, logps, index, stream)
     scratch, tp = _scratch(n, logps, stream)
-    _call(index, stream, (logps, old_logps, advantages, weights, ref_logps, out, loss, stats, scratch),
-          _entries().seqsum_policy_loss, logps.data_ptr(), n, p, dp, lp, sp, tp)
+    used = out, loss, stats, scratch, logps, old_logps, advantages, weights, ref_logps
+    try:
+        _call(index, stream, used, _entries().seqsum_policy_loss, logps.data_ptr(), n, p, dp, lp, sp, tp)
+    except SeqsumError:
+        _overlap(("out", "loss", "stats", "scratch", "logps", "old_logps", "advantages", "weights", "ref_logps"), 4, "logps", used)
+        raise
     return out, loss, stats
 
 
@@ -210,19 +223,20 @@ def token_policy_grad(logits, tokens, old_logps, advantages, weights, ref_logps=
     p = _policy(rows, index, old_logps, advantages, weights, ref_logps,
                 (clip_low, clip_high, max_ratio, kl_coef, entropy_coef, temperature))
     tp = _vector(tokens, "tokens", rows, torch.int64, index)
-    if logps is not None or entropies is not None:
-        _apart((("logps", logps), ("entropies", entropies)),
-               (("old_logps", old_logps), ("advantages", advantages), ("weights", weights), ("ref_logps", ref_logps)))
-        _apart((("logps", logps),), (("entropies", entropies),))
     out, ostride = _gradient(out, logits, stream)
     loss, lp = _result(loss, "loss", 1, logits, index, stream)
     stats, sp = _result(stats, "stats", 6, logits, index, stream)
     logps, gp = _result(logps, "logps", rows, logits, index, stream)
     entropies, ep = _result(entropies, "entropies", rows, logits, index, stream)
     scratch, cp = _scratch(rows, logits, stream)
-    _call(index, stream, (logits, tokens, old_logps, advantages, weights, ref_logps, out, loss, stats, logps, entropies, scratch),
-          _entries().seqsum_token_policy_grad, logits.data_ptr(), dtype, rows, vocab, stride, tp, p, out.data_ptr(), ostride,
-          gp, ep, lp, sp, cp)
+    used = out, loss, stats, logps, entropies, scratch, logits, tokens, old_logps, advantages, weights, ref_logps
+    try:
+        _call(index, stream, used, _entries().seqsum_token_policy_grad, logits.data_ptr(), dtype, rows, vocab, stride, tp, p,
+              out.data_ptr(), ostride, gp, ep, lp, sp, cp)
+    except SeqsumError:
+        _overlap(("out", "loss", "stats", "logps", "entropies", "scratch", "logits", "tokens", "old_logps", "advantages",
+                  "weights", "ref_logps"), 6, "logits", used)
+        raise
     return out, loss, stats, logps, entropies
 
 
@@ -293,15 +307,18 @@ def _preference_loss(logps, offsets, ref_logps, weights, settings, out, loss, sc
     rp = None if ref_logps is None else _vector(ref_logps, "ref_logps", n, f, index)
     wp = None if weights is None else _vector(weights, "weights", n, f, index)
     if grad:
-        if out is not None:
-            _apart((("out", out),), (("ref_logps", ref_logps), ("weights", weights)))
         out, dp = _result(out, "out", n, logps, index, stream)
     loss, lp = _result(loss, "loss", 1, logps, index, stream)
     scores, sp = _result(scores, "scores", 2 * pairs, logps, index, stream)
     each = _new(3 * pairs, f, logps, stream)    # the sequences' slopes, the pairs' losses
     ep = each.data_ptr()
-    _call(index, stream, (logps, offsets, ref_logps, weights, out, loss, scores, each), _entries().seqsum_preference_loss,
-          logps.data_ptr(), rp, wp, n, op, pairs, settings, dp, lp, sp, ep, ep + 8 * pairs)
+    used = out, loss, scores, each, logps, offsets, ref_logps, weights
+    try:
+        _call(index, stream, used, _entries().seqsum_preference_loss, logps.data_ptr(), rp, wp, n, op, pairs, settings, dp, lp,
+              sp, ep, ep + 8 * pairs)
+    except SeqsumError:
+        _overlap(("out", "loss", "scores", "each", "logps", "offsets", "ref_logps", "weights"), 4, "logps", used)
+        raise
     return out, loss, scores, each
 
 
