@@ -34,7 +34,7 @@ struct PairsArgs {
   const int64_t *offsets;
   int64_t pairs;
   Pair beta, margin, half_by_beta;   // the last 1 / (2 beta)
-  float smoothing, share;            // share: 1 / pairs
+  float smoothing, kept, share;      // kept: 1 - smoothing, rounded by itself; share: 1 / pairs
   int32_t kind;
   bool average;
   float *scores, *slopes, *losses;
@@ -97,9 +97,10 @@ __device__ __forceinline__ float pair_loss(const PairsArgs &a, const Pair &betwe
     slope = inside ? -a.beta.hi : beyond ? 0.0f : z.hi;
     return inside ? (1.0f - z.hi) - z.lo : beyond ? 0.0f : z.hi;
   }
-  const float e = expf(-fabsf(z.hi)), soft = log1pf(e);
-  slope = a.beta.hi * (a.smoothing - __fdiv_rn(z.hi >= 0.0f ? e : 1.0f, 1.0f + e));
-  float l = (1.0f - a.smoothing) * ((z.hi < 0.0f ? -z.hi : 0.0f) + soft);
+  // (the derivative from both sigmoids: smoothing - sigma(-z) would lose the smaller part)
+  const float e = expf(-fabsf(z.hi)), soft = log1pf(e), near = __fdiv_rn(1.0f, 1.0f + e), far = __fdiv_rn(e, 1.0f + e);
+  slope = a.beta.hi * (a.smoothing * (z.hi >= 0.0f ? near : far) - a.kept * (z.hi >= 0.0f ? far : near));
+  float l = a.kept * ((z.hi < 0.0f ? -z.hi : 0.0f) + soft);
   if (a.smoothing != 0.0f) l += a.smoothing * ((z.hi > 0.0f ? z.hi : 0.0f) + soft);
   return l;
 }
@@ -547,7 +548,7 @@ int seqsum_preference_loss(const float *logps, const float *ref_logps, const flo
               place(offsets, (2 * pairs + 1) * (int64_t)sizeof(int64_t))}))
     return SEQSUM_EINVAL;
   const PairsArgs a = {logps, ref_logps, weights, n, offsets, pairs, pair_of(s->beta), pair_of(s->margin),
-                       pair_of(0.5 / s->beta), (float)s->smoothing,
+                       pair_of(0.5 / s->beta), (float)s->smoothing, (float)(1.0 - s->smoothing),
                        pairs > 0 ? (float)(1.0 / (double)pairs) : 0.0f, s->kind,
                        s->average != 0, scores, slopes, losses, dlogps, nullptr, loss};
   return dlogps ? run_pairs<true, true>(a, stream) : run_pairs<true, false>(a, stream);
