@@ -295,10 +295,12 @@ int seqsum_tensors_clip(seqsum_tensors *tensors, float max_norm, float scale, fl
 /* ---- Losses on log-probabilities: what comes between the log-probabilities
  * above and the gradients that are clipped.
  *
- * Their sums are over tokens, and a batch's loss is often a small difference of
- * large parts, so they are carried in two floats (some 48 bits) and their order
- * goes by the number of tokens, or the lengths of the sequences, alone.  Values
- * of single tokens are fp32.  The calls enqueue on `stream` and return without
+ * A batch's loss is often a small difference of large parts: the sums of the
+ * policy term and of a sequence's score and weights are carried in two floats
+ * (some 48 bits).  The other statistics (KL, entropy, share, weight) are added
+ * in fp32 for four tokens at a time before that, and are off by some 2^-22 of
+ * their parts.  The sums' order goes by the number of tokens, or the lengths of
+ * the sequences, alone.  Values of single tokens are fp32.  The calls enqueue on `stream` and return without
  * waiting, allocate nothing, use no workspace of a stream and may be captured
  * into graphs.  What a call writes must not overlap what it reads or what else
  * it writes, but where that is said: SEQSUM_EINVAL. */
@@ -367,7 +369,10 @@ int seqsum_policy_loss_backward(const float *logps, int64_t n, const seqsum_poli
  * infinite or NaN, in masked places too.  Waits are bounded
  * as those of seqsum_token_logprob: one that gave up shows as NaN.
  *   dlogits  device, written, the logits' type; the logits themselves (with
- *            their stride) or memory apart from them
+ *            their stride) or memory apart from them.  Rows that begin at the logits'
+ *            places modulo 16 bytes are written 16 bytes at a time, others number by
+ *            number (4096 x 50257 bf16 of a buffer of 50304: 148 us, 449 to rows
+ *            without the padding)
  *   logps, entropies  device, one a row, written
  *   loss, stats  as above (stats[2]: the entropies')
  *   scratch  as above, for rows */
@@ -400,7 +405,9 @@ typedef struct {
  *   ref_logps  device, n numbers; or null: 0
  *   weights    device, n numbers (0: the token is unused, its numbers are not looked at); or null: 1
  *   offsets    device, 2 pairs + 1 numbers in order, in [0, n].  A pair whose
- *              offsets are not has NaN scores, and the loss is NaN
+ *              offsets are not has NaN scores, and the loss and the whole gradient
+ *              are NaN (and where the gradient takes logps' place, the scores of
+ *              other pairs may be of tokens that it was written over)
  *   dlogps     device, n numbers, the gradient of *loss (0 for tokens of no
  *              sequence and unused ones); may be logps itself; or null: not computed
  *   loss       device, one number (0 where there are no pairs)

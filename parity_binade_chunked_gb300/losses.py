@@ -216,9 +216,10 @@ def token_policy_grad(logits, tokens, old_logps, advantages, weights, ref_logps=
     softmax(logits / temperature); the loss is policy_loss's minus entropy_coef
     times the entropy, and stats[2] the sum of the weights times the entropies.  A
     row of weight 0, or whose token is outside [0, vocab), is unused: it is not
-    read, and its gradient, logp and entropy are 0.  `out` may be the logits.  The
-    results have no history: the gradient is there already, for
-    logits.backward(dlogits) say."""
+    read, and its gradient, logp and entropy are 0.  `out` may be the logits, or
+    rows of the logits' stride beside them (a padded buffer's, say: rows of another
+    alignment are written number by number, at a third of the speed).  The results
+    have no history: the gradient is there already, for logits.backward(dlogits) say."""
     rows, vocab, stride, dtype, index = _logits(logits)
     p = _policy(rows, index, old_logps, advantages, weights, ref_logps,
                 (clip_low, clip_high, max_ratio, kl_coef, entropy_coef, temperature))
