@@ -155,9 +155,9 @@ __device__ __forceinline__ void write_loss(const TokensArgs &a, const Sum &s, ui
 // before it is worked out, and the SMs are without a CTA for a fifth of the time (a
 // capture of 4 M tokens, half unused: 27% of DRAM, 49% of the issue slots, warps wait
 // for loads and, at the end, for the CTA's other warps).  4 M tokens with a reference
-// and gradient 26 us (101 MB; 15 at the copy rate), 1 M 11, half of 4 M unused 20.  (Two tokens an instruction; each by itself 29, 12.6 and 20.  Four
-// CTAs an SM, which spill: 30, 13.4 and 20; two: 27, 11 and 20, but 10% more from a
-// cold L2.)
+// and gradient 26 us (101 MB; 15 at the copy rate), 1 M 11, half of 4 M unused 20.
+// (Two tokens an instruction; each by itself 29, 12.6 and 20.  Four CTAs an SM, which
+// spill: 30, 13.4 and 20; two: 27, 11 and 20, but 10% more from a cold L2.)
 // A group of chunks a CTA.  kCluster: the groups are one cluster's CTAs, whose
 // first one ends the call; else finish_kernel does.
 template <bool kValue, bool kGrad, bool kCluster, int kThr>

@@ -103,3 +103,70 @@ def test_scratch_that_is_used(lib):   # noqa: F811
         for g in places:
             for address in (g << 30, (g << 30) - 49152 + 8, (g << 30) + 4 * n - 4 - 4 * n % 8):
                 assert dict(calls(lib, **k, scratch=address))[entry]() == EINVAL, (entry, g)
+
+
+# The refusals of settings and vectors again, where all vectors lie apart: what is refused is the setting or the vector.
+APART_POLICY = dict(old_logps=at(0), advantages=at(1), weights=at(2), ref_logps=at(3))
+APART_VALUE = dict(zip(("logps", "dlogps", "loss", "stats", "scratch"), (vp(at(4 + k)) for k in range(5))))
+APART_BACKWARD = dict(logps=vp(at(4)), dlogps=vp(at(5)), dloss=vp(at(9)))
+APART_ROWS = dict(zip(("logits", "tokens", "d", "logps", "entropies", "loss", "stats", "scratch"), (vp(at(10 + k)) for k in range(8))))
+APART_PAIRS = dict(zip(("logps", "ref", "weights", "offsets", "dlogps", "loss", "scores", "slopes", "losses"),
+                       (vp(at(k)) for k in range(9))))
+
+
+def odd(address):
+    """The same misplacement, at a place of its own."""
+    return at(30) + address % MIB if isinstance(address, int) else None if address is None else vp(at(30) + address.value % MIB)
+
+
+def moved(bad):
+    return {k: odd(v) if isinstance(v, vp) or v is None else v for k, v in bad.items()}
+
+
+@pytest.mark.parametrize("bad", abi.BAD_POLICIES)
+def test_policies_apart(lib, bad):   # noqa: F811
+    s = abi.policy(**{**APART_POLICY, **{k: odd(v) if k in APART_POLICY else v for k, v in bad.items()}})
+    assert abi.value(lib, s, **APART_VALUE) == abi.backward(lib, s, **APART_BACKWARD) == abi.rows(lib, s, **APART_ROWS) == EINVAL
+
+
+def bad_of(test):
+    """What an earlier test is parametrised by."""
+    return next(m.args[1] for m in test.pytestmark if m.name == "parametrize")
+
+
+@pytest.mark.parametrize("bad", bad_of(abi.test_settings_of_rows_refused))
+def test_settings_of_rows_apart(lib, bad):   # noqa: F811
+    assert abi.rows(lib, abi.policy(**APART_POLICY, **bad), **APART_ROWS) == EINVAL
+
+
+@pytest.mark.parametrize("bad", bad_of(abi.test_tokens_refused))
+def test_tokens_apart(lib, bad):   # noqa: F811
+    assert abi.value(lib, abi.policy(**APART_POLICY), **{**APART_VALUE, **moved(bad)}) == EINVAL
+
+
+@pytest.mark.parametrize("bad", bad_of(abi.test_backward_refused))
+def test_backward_apart(lib, bad):   # noqa: F811
+    assert abi.backward(lib, abi.policy(**APART_POLICY), **{**APART_BACKWARD, **moved(bad)}) == EINVAL
+
+
+@pytest.mark.parametrize("bad", [b for b in bad_of(abi.test_rows_refused) if not any(v in (abi.P, abi.Q) for v in b.values())
+                                 and not ("logps" in b and "entropies" in b)])
+def test_rows_apart(lib, bad):   # noqa: F811
+    assert abi.rows(lib, abi.policy(**APART_POLICY), **{**APART_ROWS, **moved(bad)}) == EINVAL
+
+
+@pytest.mark.parametrize("bad", bad_of(abi.test_preferences_refused))
+def test_preferences_apart(lib, bad):   # noqa: F811
+    assert abi.pairs(lib, abi.preference(**bad), **APART_PAIRS) == EINVAL
+
+
+@pytest.mark.parametrize("bad", bad_of(abi.test_pairs_refused))
+def test_pairs_apart(lib, bad):   # noqa: F811
+    assert abi.pairs(lib, abi.preference(), **{**APART_PAIRS, **moved(bad)}) == EINVAL
+
+
+@pytest.mark.parametrize("bad", bad_of(abi.test_preference_backward_refused))
+def test_preference_backward_apart(lib, bad):   # noqa: F811
+    a = {**dict(weights=vp(at(0)), n=100, offsets=vp(at(1)), k=3, slopes=vp(at(2)), dloss=vp(at(3)), dlogps=vp(at(4))), **moved(bad)}
+    assert lib.seqsum_preference_backward(a["weights"], i64(a["n"]), a["offsets"], i64(a["k"]), a["slopes"], a["dloss"],
+                                          a["dlogps"], None) == EINVAL
