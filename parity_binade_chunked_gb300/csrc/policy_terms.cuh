@@ -139,9 +139,10 @@ struct Policy {
 
 // e^x - 1 - x, m = e^x - 1 and r = e^x.  For |x| < 1 by its series (the first term
 // left out is 2 / 13! of the sum), where none loses digits to a difference, and r
-// comes with what its rounding and m's left out; elsewhere without inf - inf.
-template <typename V>
-__device__ __forceinline__ V excess(V x, V &m, V &r, V &r_rest) {
+// comes with what its rounding and m's left out; elsewhere without inf - inf, and r
+// is far(r).
+template <typename V, typename F>
+__device__ __forceinline__ V excess(V x, V &m, V &r, V &r_rest, F far) {
   V p = splat<V>(1.0f / 479001600.0f);
   p = fma(p, x, splat<V>(1.0f / 39916800.0f));
   p = fma(p, x, splat<V>(1.0f / 3628800.0f));
@@ -160,7 +161,7 @@ __device__ __forceinline__ V excess(V x, V &m, V &r, V &r_rest) {
   const auto near = test(x, [](float v) { return fabsf(v) < 1.0f; });
   if (!all(near)) {
     m = pick(near, m, each(x, [](float v) { return expm1f(v); }));
-    r = pick(near, r, each(x, [](float v) { return expf(v); }));
+    r = pick(near, r, far(each(x, [](float v) { return expf(v); })));
     r_rest = pick(near, r_rest, splat<V>(0.0f));
     k = pick(near, k, sub(m, each(x, [](float v) { return fminf(v, 3.40282347e38f); })));
   }
@@ -191,7 +192,11 @@ __device__ __forceinline__ Terms<V> policy_terms(const Policy &p, V logp, V old,
   const auto past = either(above, below);
   Terms<V> t;
   V m, ratio, ratio_rest;
-  t.old_kl = excess(d, m, ratio, ratio_rest);
+  t.old_kl = excess(d, m, ratio, ratio_rest, [&](V r) {
+    // an advantage of 0 leaves nothing of a ratio beyond fp32 either, where no bound has met that
+    return pick(unless(test(r, [](float v) { return v == INFINITY; }), test(advantage, [](float v) { return v != 0.0f; })),
+                splat<V>(3.40282347e38f), r);
+  });
   const V f = pick(past, pick(below, splat<V>(p.down), of(p.up, p.top)), ratio),
           f_rest = pick(past, pick(below, splat<V>(p.down_rest), of(p.up_rest, p.top_rest)), fma(ratio, e, ratio_rest));
   const V loss = sub(zero, advantage);
@@ -202,7 +207,7 @@ __device__ __forceinline__ Terms<V> policy_terms(const Policy &p, V logp, V old,
   t.kl = zero;
   if (p.ref_logps) {
     V unused;
-    t.kl = excess(sub(ref, logp), m, unused, unused);
+    t.kl = excess(sub(ref, logp), m, unused, unused, [](V r) { return r; });
     if (p.kl_coef != 0.0f) t.slope = sub(t.slope, mul(splat<V>(p.kl_coef), m));
   }
   return t;
