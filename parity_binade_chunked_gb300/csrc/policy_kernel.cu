@@ -329,9 +329,11 @@ bool take_policy(const seqsum_policy *s, int64_t n, bool rows, Policy *to) {
   if (rows && !(s->temperature >= 1e-30 && s->temperature <= 1e30)) return false;
   if (n > 0 && (!s->old_logps || !s->advantages || !s->weights)) return false;
   if (misplaced(s->old_logps) || misplaced(s->advantages) || misplaced(s->weights) || misplaced(s->ref_logps)) return false;
-  const double up = 1.0 + s->clip_high, down = 1.0 - s->clip_low;
-  *to = {s->old_logps, s->advantages, s->weights, s->ref_logps, (float)up, (float)down, (float)s->max_ratio, rest_of(up),
-         rest_of(down), rest_of(s->max_ratio), bound_of(up), bound_of(down), bound_of(s->max_ratio),
+  // (a bound beyond fp32 is none)
+  auto within = [](double x) { return isfinite((float)x) ? x : (double)INFINITY; };
+  const double up = within(1.0 + s->clip_high), down = 1.0 - s->clip_low, top = within(s->max_ratio);
+  *to = {s->old_logps, s->advantages, s->weights, s->ref_logps, (float)up, (float)down, (float)top, rest_of(up),
+         rest_of(down), rest_of(top), bound_of(up), bound_of(down), bound_of(top),
          (float)s->kl_coef, rows ? (float)s->entropy_coef : 0.0f, rows ? (float)(1.0 / s->temperature) : 1.0f};
   return true;
 }

@@ -49,3 +49,14 @@ def test_rows(sq, dtype, vocab):
     t, w = torch.zeros(3, dtype=torch.int64, device="cuda"), torch.ones(3, device="cuda")
     d, loss, stats, logps, _ = sq.token_policy_grad(x, t, torch.full((3,), -200.0, device="cuda"), 0 * w, w, **OPEN)
     assert loss.item() == 0 and stats[0].item() == 0 and not d.any() and logps.isfinite().all()
+
+
+@pytest.mark.parametrize("clip_high", [1e39, 1e300])
+def test_bounds_beyond_fp32(sq, clip_high):
+    """Such a bound is none: 0 times it is 0."""
+    logps = torch.full((5,), -1.0, device="cuda")
+    old, w, a = logps - 800.0, torch.ones(5, device="cuda"), torch.zeros(5, device="cuda")
+    d, loss, stats = sq.policy_loss_grad(logps, old, a, w, clip_high=clip_high, max_ratio=clip_high)
+    assert loss.item() == 0 and stats[3].item() == 0 and not d.any()
+    d, loss, _ = sq.policy_loss_grad(logps, old, a + 1, w, clip_high=clip_high)
+    assert loss.item() == -math.inf and (d == -math.inf).all()
