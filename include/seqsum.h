@@ -316,7 +316,7 @@ int seqsum_tensors_clip(seqsum_tensors *tensors, float max_norm, float scale, fl
 /* The settings of the policy losses, and what stands beside each token. */
 typedef struct {
   double clip_low;            /* the ratio's lower bound is 1 - clip_low (0 to 1) */
-  double clip_high;           /* its upper bound 1 + clip_high (>= 0) */
+  double clip_high;           /* its upper bound 1 + clip_high (>= 0; infinity, or beyond fp32: none) */
   double max_ratio;           /* its upper bound where the advantage is negative (>= 1; infinity: none) */
   double kl_coef;
   double entropy_coef;        /* seqsum_token_policy_grad only */
